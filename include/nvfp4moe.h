@@ -461,8 +461,8 @@ NVFP4MOE_API int nvfp4moe_status_read(const void* ws, void* stream);
 NVFP4MOE_API const char* nvfp4moe_status_string(int status);
 
 /* Waits for `stream`, then returns the device-side status of the last call on this host
- * thread that enqueued work with a status word: the quantize, route, forward and FP8 calls
- * (their workspace's word) and nvfp4moe_route_noalloc (the word of the library's fixed
+ * thread that enqueued work with a status word: the quantize, route, forward, FP8 and product
+ * calls (their workspace's word) and nvfp4moe_route_noalloc (the word of the library's fixed
  * scratch, which only this call can read).  Same results as nvfp4moe_status_read; also
  * NVFP4MOE_ERR_ARG when no such call has been made on this thread.  The workspace that call
  * used must still be allocated. */
@@ -546,8 +546,104 @@ NVFP4MOE_API int nvfp4moe_forward_fp8(const nvfp4moe_fp8_experts* experts, const
                                       const float* w_router, const float* logit_bias, void* out_bf16,
                                       const nvfp4moe_debug* dbg, void* ws, size_t ws_bytes, void* stream);
 
+/* --------------------------------------------------- 16-bit products and norm ----
+ * The 16-bit side of the layer: what the checkpoint keeps in BF16 (norms, dense MLPs) and the
+ * experts before they are quantised, forward and backward, for calibration, for comparison with
+ * the quantised layer and for training.  The conventions of the file header hold (device
+ * pointers, dense row-major tensors, errors, status word, workspaces).  Tensor pointers are
+ * 16-byte aligned unless stated otherwise, and outputs do not overlap inputs unless stated.
+ *
+ * Products take BF16 or FP16 operands, accumulate in FP32 on the tensor cores and round each
+ * result once.  Limits: 0 <= M < 2^30, K and N multiples of 8 from 8 to 2^19, 1 <= E <= 1024,
+ * M * K, M * N and E * K * N below 2^40; outside them NVFP4MOE_ERR_SHAPE. */
+enum { NVFP4MOE_BF16 = 0, NVFP4MOE_FP16 = 1, NVFP4MOE_FP32 = 2 };   /* element types */
+
+/* Activations: RELU max(z, 0); SILU z / (1 + exp(-z)); GELU z (1 + erf(z / sqrt 2)) / 2;
+ * GELU_TANH z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2. */
+enum {
+  NVFP4MOE_ACT_NONE = 0,
+  NVFP4MOE_ACT_RELU = 1,
+  NVFP4MOE_ACT_SILU = 2,
+  NVFP4MOE_ACT_GELU = 3,
+  NVFP4MOE_ACT_GELU_TANH = 4
+};
+
+/* Products grouped by expert: y[i] = x[i] W_e^T for the rows offsets[e] <= i < offsets[e+1].
+ *
+ *   dtype    NVFP4MOE_BF16 or NVFP4MOE_FP16, the type of x, w and y
+ *   x        [M][K];  w [E][N][K];  y out [M][N]
+ *   offsets  [E+1] int32 (4-byte aligned), device: nondecreasing, 0 <= offsets[0],
+ *            offsets[E] <= M (dbg->offsets of nvfp4moe_forward has this form).  Segments may be
+ *            empty and need no alignment.  Rows outside offsets[0] .. offsets[E] are neither used nor
+ *            written.  Offsets that break the rule raise NVFP4MOE_ERR_ARG in the status word; every
+ *            segment then counts as empty.
+ *   ws       nvfp4moe_grouped_mm_workspace_bytes(E) bytes
+ *
+ * nvfp4moe_grouped_mm_backward, with dy [M][N] the gradient of y:
+ *   dx       out [M][K] or NULL: dx[i] = dy[i] W_e (rows outside the segments are not written)
+ *   dw       out [E][N][K] or NULL: dW_e = sum over the segment's rows of dy[i]^T x[i], zero for an
+ *            empty segment; dw_dtype is dtype or NVFP4MOE_FP32
+ *   x may be NULL without dw, w without dx; dx and dw not both NULL (else NVFP4MOE_ERR_ARG).
+ *   Values outside the segments never enter a sum, whatever they are. */
+NVFP4MOE_API size_t nvfp4moe_grouped_mm_workspace_bytes(int32_t E);
+NVFP4MOE_API int nvfp4moe_grouped_mm(int32_t dtype, const void* x, int64_t M, int32_t K, const void* w, int32_t E,
+                                     int32_t N, const int32_t* offsets, void* y, void* ws, size_t ws_bytes,
+                                     void* stream);
+NVFP4MOE_API int nvfp4moe_grouped_mm_backward(int32_t dtype, const void* dy, const void* x, const void* w, int64_t M,
+                                              int32_t K, int32_t E, int32_t N, const int32_t* offsets, void* dx,
+                                              void* dw, int32_t dw_dtype, void* ws, size_t ws_bytes, void* stream);
+
+/* Dense product with its epilogue: z = x W^T + bias, y = act(z) + residual, all in FP32 with one
+ * rounding of y.
+ *
+ *   x [M][K], w [N][K], y out [M][N] of type dtype (BF16 or FP16);  bias [N] FP32 or NULL;
+ *   residual [M][N] of type dtype or NULL, may be y itself (in-place update of a stream);
+ *   z_out out [M][N] of type dtype or NULL: z rounded, for the backward pass.
+ *
+ * nvfp4moe_linear_backward, with dy [M][N] the gradient of y and z as z_out saved it (may be NULL
+ * without an activation); the gradient of residual is dy itself:
+ *   dz = dy act'(z) in FP32, rounded to dtype as the operand of the two products (dy itself
+ *        without an activation)
+ *   dx  out [M][K] or NULL: dz W;   dw out [N][K] or NULL: dz^T x, dw_dtype as above;
+ *   db  out [N] FP32 or NULL: the column sums of the unrounded dz.
+ *   At least one of dx, dw, db; x may be NULL without dw, w without dx.
+ * M = 0 leaves nothing to do forward; backward it writes zeros to dw and db. */
+NVFP4MOE_API size_t nvfp4moe_linear_workspace_bytes(int64_t M, int32_t K, int32_t N);
+NVFP4MOE_API int nvfp4moe_linear(int32_t dtype, const void* x, int64_t M, int32_t K, const void* w, int32_t N,
+                                 const float* bias, int32_t act, const void* residual, void* z_out, void* y, void* ws,
+                                 size_t ws_bytes, void* stream);
+NVFP4MOE_API size_t nvfp4moe_linear_backward_workspace_bytes(int64_t M, int32_t K, int32_t N);
+NVFP4MOE_API int nvfp4moe_linear_backward(int32_t dtype, const void* dy, const void* x, const void* w, const void* z,
+                                          int64_t M, int32_t K, int32_t N, int32_t act, void* dx, void* dw,
+                                          int32_t dw_dtype, float* db, void* ws, size_t ws_bytes, void* stream);
+
+/* Layer norm over the rows of x [rows][cols] (any cols from 1 to 28672, 0 <= rows < 2^31), type BF16,
+ * FP16 or FP32, arithmetic and parameters FP32:
+ *   y = (x - mean) rstd gamma + beta,   rstd = 1 / sqrt(mean_j((x - mean)^2) + eps)
+ * or, with rms != 0, y = x rstd gamma, rstd = 1 / sqrt(mean_j(x^2) + eps) (beta must be NULL).
+ *
+ *   gamma, beta [cols] FP32 or NULL (ones, zeros), 4-byte aligned;  eps >= 0;
+ *   y out, may be x itself;  mean, rstd out [rows] FP32 or NULL (mean is not written with rms).
+ * Writes no status word and takes no workspace.
+ *
+ * nvfp4moe_layer_norm_backward, with dy the gradient of y and mean (NULL with rms) and rstd of the
+ * forward call, xh = (x - mean) rstd, g = dy gamma:
+ *   dx = rstd (g - mean_j(g) - xh mean_j(g xh))   (rms: without mean_j(g)); may be dy itself
+ *   dgamma out [cols] FP32 or NULL: sum over rows of dy xh;  dbeta out [cols] FP32 or NULL: sum
+ *   of dy (NULL with rms).  The sums run in an order fixed by the shape.  rows = 0 writes zeros.
+ *   ws  nvfp4moe_layer_norm_backward_workspace_bytes(rows, cols) bytes; may be NULL (0 bytes)
+ *       without dgamma and dbeta.  Holds no status word. */
+NVFP4MOE_API int nvfp4moe_layer_norm(int32_t dtype, const void* x, int64_t rows, int32_t cols, const float* gamma,
+                                     const float* beta, float eps, int32_t rms, void* y, float* mean, float* rstd,
+                                     void* stream);
+NVFP4MOE_API size_t nvfp4moe_layer_norm_backward_workspace_bytes(int64_t rows, int32_t cols);
+NVFP4MOE_API int nvfp4moe_layer_norm_backward(int32_t dtype, const void* dy, const void* x, int64_t rows, int32_t cols,
+                                              const float* gamma, const float* mean, const float* rstd, int32_t rms,
+                                              void* dx, float* dgamma, float* dbeta, void* ws, size_t ws_bytes,
+                                              void* stream);
+
 /* Number of kernels enqueued by the last call on this host thread that enqueues work
- * (the quantize, route, experts_set, forward and finalize families; nvfp4moe_route_noalloc
+ * (the quantize, route, experts_set, forward, finalize, product and norm families; nvfp4moe_route_noalloc
  * leaves the count unchanged), for launch accounting in benchmarks.  A call that returns an
  * error before enqueuing anything reports 0. */
 NVFP4MOE_API int32_t nvfp4moe_last_launch_count(void);

@@ -23,12 +23,19 @@ weighted residual add out), ``quantize_weights_lh`` (local-Hessian weight scales
 a gather exchange, the same with the combine into the owners' memory inside the down GEMM, or an
 all-to-all one), and ``tp.TensorParallelLayer`` (every expert's intermediate features split over
 the ranks, an all-reduce of the FP32 sums).
+
+The layer's 16-bit side, forward and backward (norms, dense products, experts before they are
+quantised): ``layer_norm`` / ``layer_norm_backward``, ``linear`` / ``linear_backward`` (bias, activation
+and residual in the product's epilogue), ``grouped_mm`` / ``grouped_mm_backward`` (products grouped by
+expert with ragged sizes).
 """
 from ._lib import (  # noqa: F401
     Cfg, Experts, NvFp4MoeError, cfg_default, make_cfg, quantize, quantize_weights_lh, route, route_noalloc, forward,
     forward_residual, status_read, last_device_status, workspace_bytes, quantize_fp8, Fp8Experts, forward_fp8, forward_fp8_workspace_bytes,
     forward_partial, finalize, amax, ep_dispatch, ep_dispatch_workspace_bytes, ep_experts, ep_experts_workspace_bytes,
     ep_combine, forward_partial_peer, ipc_handle, ipc_open, ipc_close,
+    grouped_mm, grouped_mm_backward, grouped_mm_workspace_bytes, linear, linear_backward, linear_workspace_bytes,
+    linear_backward_workspace_bytes, layer_norm, layer_norm_backward, layer_norm_backward_workspace_bytes,
     status_string, last_launch_count, forward_workspace_bytes, route_workspace_bytes,
     quantize_workspace_bytes, swizzled_scale_bytes, declared_symbols, lib, LIB_PATH, StageTimer, STAGES,
     OK, ERR_ARG, ERR_SHAPE, ERR_CUDA, ERR_WORKSPACE, ERR_NONFINITE, ERR_TIMEOUT, ERR_DEVICE,

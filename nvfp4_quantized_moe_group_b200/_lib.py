@@ -140,6 +140,22 @@ _SIGS = {
     "nvfp4moe_ep_experts_workspace_bytes": (_SZ, [ctypes.POINTER(Cfg), ctypes.c_int32, _I64]),
     "nvfp4moe_ep_experts": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _P, _P, _P, _SZ, _P]),
     "nvfp4moe_ep_combine": (ctypes.c_int, [_P, _P, _I64, ctypes.c_int32, ctypes.c_int32, _P, _P]),
+    "nvfp4moe_grouped_mm_workspace_bytes": (_SZ, [ctypes.c_int32]),
+    "nvfp4moe_grouped_mm": (ctypes.c_int, [ctypes.c_int32, _P, _I64, ctypes.c_int32, _P, ctypes.c_int32,
+                                           ctypes.c_int32, _P, _P, _P, _SZ, _P]),
+    "nvfp4moe_grouped_mm_backward": (ctypes.c_int, [ctypes.c_int32, _P, _P, _P, _I64, ctypes.c_int32, ctypes.c_int32,
+                                                    ctypes.c_int32, _P, _P, _P, ctypes.c_int32, _P, _SZ, _P]),
+    "nvfp4moe_linear_workspace_bytes": (_SZ, [_I64, ctypes.c_int32, ctypes.c_int32]),
+    "nvfp4moe_linear": (ctypes.c_int, [ctypes.c_int32, _P, _I64, ctypes.c_int32, _P, ctypes.c_int32, _P,
+                                       ctypes.c_int32, _P, _P, _P, _P, _SZ, _P]),
+    "nvfp4moe_linear_backward_workspace_bytes": (_SZ, [_I64, ctypes.c_int32, ctypes.c_int32]),
+    "nvfp4moe_linear_backward": (ctypes.c_int, [ctypes.c_int32, _P, _P, _P, _P, _I64, ctypes.c_int32, ctypes.c_int32,
+                                                ctypes.c_int32, _P, _P, ctypes.c_int32, _P, _P, _SZ, _P]),
+    "nvfp4moe_layer_norm": (ctypes.c_int, [ctypes.c_int32, _P, _I64, ctypes.c_int32, _P, _P, ctypes.c_float,
+                                           ctypes.c_int32, _P, _P, _P, _P]),
+    "nvfp4moe_layer_norm_backward_workspace_bytes": (_SZ, [_I64, ctypes.c_int32]),
+    "nvfp4moe_layer_norm_backward": (ctypes.c_int, [ctypes.c_int32, _P, _P, _I64, ctypes.c_int32, _P, _P, _P,
+                                                    ctypes.c_int32, _P, _P, _P, _P, _SZ, _P]),
     "nvfp4moe_status_read": (ctypes.c_int, [_P, _P]),
     "nvfp4moe_last_device_status": (ctypes.c_int, [_P]),
     "nvfp4moe_workspace_bytes": (_SZ, [ctypes.POINTER(Cfg), _I64]),
@@ -783,3 +799,205 @@ def ep_combine(rows: torch.Tensor, pos: torch.Tensor, T: int, topk: int, out: to
     _check(lib().nvfp4moe_ep_combine(_ptr(rows), _ptr(pos), int(T), int(topk), H, _ptr(out), _stream(stream)),
            "nvfp4moe_ep_combine")
     return out
+
+
+# ------------------------------------------------------------- 16-bit products and norm ----
+
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+
+
+def _dtype_of(t, name: str, allowed) -> torch.dtype:
+    if not isinstance(t, torch.Tensor) or t.dtype not in allowed:
+        raise TypeError(f"{name} must be a tensor of one of {', '.join(str(d) for d in allowed)}, got "
+                        f"{t.dtype if isinstance(t, torch.Tensor) else type(t).__name__}")
+    return t.dtype
+
+
+_HALF = (torch.bfloat16, torch.float16)
+
+
+def _activation(act: str) -> int:
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}, got {act!r}")
+    return ACTIVATIONS[act]
+
+
+def _dw_dtype(dw_dtype, dt) -> torch.dtype:
+    if dw_dtype is None:
+        return dt
+    if dw_dtype not in (dt, torch.float32):
+        raise TypeError(f"dw_dtype must be {dt} or torch.float32, got {dw_dtype}")
+    return dw_dtype
+
+
+def grouped_mm_workspace_bytes(E: int) -> int:
+    return int(lib().nvfp4moe_grouped_mm_workspace_bytes(int(E)))
+
+
+def grouped_mm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, out: torch.Tensor | None = None, ws=None,
+               stream=None) -> torch.Tensor:
+    """Products grouped by expert (nvfp4moe_grouped_mm): x [M, K] bf16 or fp16, w [E, N, K],
+    offsets [E + 1] int32 -> y [M, N], y[i] = x[i] w[e]^T for offsets[e] <= i < offsets[e + 1].
+    Rows outside the segments are not written (unspecified when ``out`` is not given)."""
+    dt = _dtype_of(x, "x", _HALF)
+    M = _rows(x, "x", min_rows=0)
+    K = int(x.shape[1])
+    if not isinstance(w, torch.Tensor) or w.dim() != 3:
+        raise TypeError("w must be a 3-D tensor")
+    E, N = int(w.shape[0]), int(w.shape[1])
+    _require((x, "x", dt, None), (w, "w", dt, (E, N, K)), (offsets, "offsets", torch.int32, (E + 1,)),
+             (out, "out", dt, (M, N)), (ws, "ws", torch.uint8, None))
+    if out is None:
+        out = torch.empty((M, N), dtype=dt, device=x.device)
+    if ws is None:
+        ws = _workspace(grouped_mm_workspace_bytes(E), x.device)
+    _check(lib().nvfp4moe_grouped_mm(DTYPES[dt], _ptr(x), M, K, _ptr(w), E, N, _ptr(offsets), _ptr(out), _ptr(ws),
+                                     ws.numel(), _stream(stream)), "nvfp4moe_grouped_mm")
+    return out
+
+
+def grouped_mm_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
+                        need_dx: bool = True, need_dw: bool = True, dw_dtype: torch.dtype | None = None,
+                        dx: torch.Tensor | None = None, dw: torch.Tensor | None = None, ws=None, stream=None):
+    """Gradients of grouped_mm (nvfp4moe_grouped_mm_backward): dy [M, N] -> (dx [M, K], dw [E, N, K]),
+    None for the one not needed.  ``dx`` / ``dw``: where to write them; ``dw_dtype``: the type of a
+    new dw (x's, or torch.float32)."""
+    dt = _dtype_of(dy, "dy", _HALF)
+    M = _rows(dy, "dy", min_rows=0)
+    N = int(dy.shape[1])
+    if not isinstance(w, torch.Tensor) or w.dim() != 3:
+        raise TypeError("w must be a 3-D tensor")
+    E, K = int(w.shape[0]), int(w.shape[2])
+    wt = _dw_dtype(dw.dtype if isinstance(dw, torch.Tensor) and dw_dtype is None else dw_dtype, dt)
+    _require((dy, "dy", dt, None), (x, "x", dt, (M, K)), (w, "w", dt, (E, N, K)),
+             (offsets, "offsets", torch.int32, (E + 1,)), (dx, "dx", dt, (M, K)), (dw, "dw", wt, (E, N, K)),
+             (ws, "ws", torch.uint8, None))
+    if dx is None and need_dx:
+        dx = torch.empty((M, K), dtype=dt, device=dy.device)
+    if dw is None and need_dw:
+        dw = torch.empty((E, N, K), dtype=wt, device=dy.device)
+    if ws is None:
+        ws = _workspace(grouped_mm_workspace_bytes(E), dy.device)
+    _check(lib().nvfp4moe_grouped_mm_backward(DTYPES[dt], _ptr(dy), _ptr(x), _ptr(w), M, K, E, N, _ptr(offsets),
+                                              _ptr(dx), _ptr(dw), DTYPES[wt], _ptr(ws), ws.numel(), _stream(stream)),
+           "nvfp4moe_grouped_mm_backward")
+    return dx, dw
+
+
+def linear_workspace_bytes(M: int, K: int, N: int) -> int:
+    return int(lib().nvfp4moe_linear_workspace_bytes(int(M), int(K), int(N)))
+
+
+def linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None, act: str = "none",
+           residual: torch.Tensor | None = None, save_z: bool = False, out: torch.Tensor | None = None, ws=None,
+           stream=None):
+    """Dense product with its epilogue (nvfp4moe_linear): x [M, K] bf16 or fp16, w [N, K],
+    bias [N] float32, residual [M, N] -> act(x w^T + bias) + residual [M, N], rounded once.
+    ``act``: none, relu, silu, gelu or gelu_tanh.  ``save_z``: also return the rounded
+    pre-activation for linear_backward.  ``out`` may be ``residual`` (in-place update)."""
+    dt = _dtype_of(x, "x", _HALF)
+    a = _activation(act)
+    M = _rows(x, "x", min_rows=0)
+    K = int(x.shape[1])
+    N = _rows(w, "w")
+    _require((x, "x", dt, None), (w, "w", dt, (N, K)), (bias, "bias", torch.float32, (N,)),
+             (residual, "residual", dt, (M, N)), (out, "out", dt, (M, N)), (ws, "ws", torch.uint8, None))
+    if out is None:
+        out = torch.empty((M, N), dtype=dt, device=x.device)
+    z = torch.empty((M, N), dtype=dt, device=x.device) if save_z else None
+    if ws is None:
+        ws = _workspace(linear_workspace_bytes(M, K, N), x.device)
+    _check(lib().nvfp4moe_linear(DTYPES[dt], _ptr(x), M, K, _ptr(w), N, _ptr(bias), a, _ptr(residual), _ptr(z),
+                                 _ptr(out), _ptr(ws), ws.numel(), _stream(stream)), "nvfp4moe_linear")
+    return (out, z) if save_z else out
+
+
+def linear_backward_workspace_bytes(M: int, K: int, N: int) -> int:
+    return int(lib().nvfp4moe_linear_backward_workspace_bytes(int(M), int(K), int(N)))
+
+
+def linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, z: torch.Tensor | None = None,
+                    act: str = "none", bias: bool = False, need_dx: bool = True, need_dw: bool = True,
+                    dw_dtype: torch.dtype | None = None, dx: torch.Tensor | None = None,
+                    dw: torch.Tensor | None = None, ws=None, stream=None):
+    """Gradients of linear (nvfp4moe_linear_backward): dy [M, N] and the saved pre-activation z ->
+    (dx [M, K], dw [N, K], db [N] float32), None for those not needed (``bias``: db is).  The
+    gradient of the residual is dy."""
+    dt = _dtype_of(dy, "dy", _HALF)
+    a = _activation(act)
+    if a != 0 and z is None:
+        raise ValueError(f"act {act!r} needs the pre-activation z")
+    M = _rows(dy, "dy", min_rows=0)
+    N = int(dy.shape[1])
+    K = int(w.shape[1]) if _rows(w, "w") else 0
+    wt = _dw_dtype(dw.dtype if isinstance(dw, torch.Tensor) and dw_dtype is None else dw_dtype, dt)
+    _require((dy, "dy", dt, None), (x, "x", dt, (M, K)), (w, "w", dt, (N, K)), (z, "z", dt, (M, N)),
+             (dx, "dx", dt, (M, K)), (dw, "dw", wt, (N, K)), (ws, "ws", torch.uint8, None))
+    dev = dy.device
+    if dx is None and need_dx:
+        dx = torch.empty((M, K), dtype=dt, device=dev)
+    if dw is None and need_dw:
+        dw = torch.empty((N, K), dtype=wt, device=dev)
+    db = torch.empty(N, dtype=torch.float32, device=dev) if bias else None
+    if ws is None:
+        ws = _workspace(linear_backward_workspace_bytes(M, K, N), dev)
+    _check(lib().nvfp4moe_linear_backward(DTYPES[dt], _ptr(dy), _ptr(x), _ptr(w), _ptr(z), M, K, N, a, _ptr(dx),
+                                          _ptr(dw), DTYPES[wt], _ptr(db), _ptr(ws), ws.numel(), _stream(stream)),
+           "nvfp4moe_linear_backward")
+    return dx, dw, db
+
+
+def layer_norm(x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.Tensor | None = None,
+               eps: float = 1e-5, rms: bool = False, stats: bool = False, out: torch.Tensor | None = None,
+               stream=None):
+    """Layer norm of the rows of x [rows, cols] bf16, fp16 or fp32 (nvfp4moe_layer_norm), or with
+    ``rms`` its RMS form; gamma, beta [cols] float32.  ``out`` may be ``x``.  ``stats``: return
+    (y, mean, rstd) for layer_norm_backward (mean None with rms)."""
+    dt = _dtype_of(x, "x", tuple(DTYPES))
+    rows = _rows(x, "x", min_rows=0)
+    cols = int(x.shape[1])
+    _require((x, "x", dt, None), (gamma, "gamma", torch.float32, (cols,)), (beta, "beta", torch.float32, (cols,)),
+             (out, "out", dt, (rows, cols)))
+    if out is None:
+        out = torch.empty_like(x)
+    mean = torch.empty(rows, dtype=torch.float32, device=x.device) if stats and not rms else None
+    rstd = torch.empty(rows, dtype=torch.float32, device=x.device) if stats else None
+    _check(lib().nvfp4moe_layer_norm(DTYPES[dt], _ptr(x), rows, cols, _ptr(gamma), _ptr(beta), float(eps),
+                                     int(bool(rms)), _ptr(out), _ptr(mean), _ptr(rstd), _stream(stream)),
+           "nvfp4moe_layer_norm")
+    return (out, mean, rstd) if stats else out
+
+
+def layer_norm_backward_workspace_bytes(rows: int, cols: int) -> int:
+    return int(lib().nvfp4moe_layer_norm_backward_workspace_bytes(int(rows), int(cols)))
+
+
+def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor | None, mean: torch.Tensor | None,
+                        rstd: torch.Tensor, rms: bool = False, need_params: bool | None = None,
+                        dx: torch.Tensor | None = None, ws=None, stream=None):
+    """Gradients of layer_norm (nvfp4moe_layer_norm_backward): (dx, dgamma [cols], dbeta [cols]), the
+    parameters' in float32, dbeta None with rms.  ``need_params``: whether dgamma and dbeta are
+    computed (default: when gamma is given; None otherwise).  ``dx`` may be ``dy``."""
+    dt = _dtype_of(dy, "dy", tuple(DTYPES))
+    rows = _rows(dy, "dy", min_rows=0)
+    cols = int(dy.shape[1])
+    if not rms and mean is None:
+        raise ValueError("the layer form needs the mean of the forward pass")
+    _require((dy, "dy", dt, None), (x, "x", dt, (rows, cols)), (gamma, "gamma", torch.float32, (cols,)),
+             (mean, "mean", torch.float32, (rows,)), (rstd, "rstd", torch.float32, (rows,)),
+             (dx, "dx", dt, (rows, cols)), (ws, "ws", torch.uint8, None))
+    dev = dy.device
+    if need_params is None:
+        need_params = gamma is not None
+    if dx is None:
+        dx = torch.empty_like(dy)
+    dgamma = torch.empty(cols, dtype=torch.float32, device=dev) if need_params else None
+    dbeta = torch.empty(cols, dtype=torch.float32, device=dev) if need_params and not rms else None
+    if ws is None and need_params:
+        ws = _workspace(layer_norm_backward_workspace_bytes(rows, cols), dev)
+    _check(lib().nvfp4moe_layer_norm_backward(DTYPES[dt], _ptr(dy), _ptr(x), rows, cols, _ptr(gamma),
+                                              None if rms else _ptr(mean), _ptr(rstd), int(bool(rms)), _ptr(dx),
+                                              _ptr(dgamma), _ptr(dbeta), _ptr(ws), ws.numel() if ws is not None else 0,
+                                              _stream(stream)), "nvfp4moe_layer_norm_backward")
+    return dx, dgamma, dbeta

@@ -1,0 +1,67 @@
+// Activations of the dense product and their derivatives, in FP32.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "nvfp4moe.h"
+
+namespace nvfp4moe {
+
+constexpr float kSqrtHalf = 0.70710678118654752f;
+constexpr float kInvSqrt2Pi = 0.39894228040143268f;
+constexpr float kSqrt2OverPi = 0.79788456080286536f;
+
+// 1 / (1 + exp(-z)); exp(-z) = inf gives 0.
+__device__ __forceinline__ float sigmoid_f(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+
+// NaN stays NaN in every activation.
+__device__ __forceinline__ float act_value(float z, int act) {
+  switch (act) {
+    case NVFP4MOE_ACT_RELU: return z < 0.0f ? 0.0f : z;
+    case NVFP4MOE_ACT_SILU: return z * sigmoid_f(z);
+    case NVFP4MOE_ACT_GELU: return 0.5f * z * (1.0f + erff(z * kSqrtHalf));
+    // 0.5 (1 + tanh(u)) = 1 / (1 + exp(-2u))
+    case NVFP4MOE_ACT_GELU_TANH: return z * sigmoid_f(2.0f * kSqrt2OverPi * (z + 0.044715f * z * z * z));
+    default: return z;
+  }
+}
+
+// d act / dz
+__device__ __forceinline__ float act_slope(float z, int act) {
+  switch (act) {
+    case NVFP4MOE_ACT_RELU: return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
+    case NVFP4MOE_ACT_SILU: {
+      const float p = sigmoid_f(z);
+      return p * (1.0f + z * (1.0f - p));
+    }
+    case NVFP4MOE_ACT_GELU:
+      return 0.5f * (1.0f + erff(z * kSqrtHalf)) + z * __expf(-0.5f * z * z) * kInvSqrt2Pi;
+    case NVFP4MOE_ACT_GELU_TANH: {
+      const float z2 = z * z;
+      const float p = sigmoid_f(2.0f * kSqrt2OverPi * (z + 0.044715f * z * z2));
+      // p + z p (1 - p) d(2u)/dz; far out the second term's first factors are 0 and z2 may be inf
+      const float q = z * p * (1.0f - p);
+      return q == 0.0f ? p : p + q * (2.0f * kSqrt2OverPi) * (1.0f + 3.0f * 0.044715f * z2);
+    }
+    default: return 1.0f;
+  }
+}
+
+// Two FP32 -> two 16-bit values in one word (lo in the low half), round to nearest even.
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, bool fp16) {
+  if (fp16) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+__device__ __forceinline__ float2 unpack16(uint32_t w, bool fp16) {
+  if (fp16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+}  // namespace nvfp4moe

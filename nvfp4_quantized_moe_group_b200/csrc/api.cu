@@ -5,7 +5,9 @@
 #include <vector>
 
 #include "common.cuh"
+#include "dense.h"
 #include "kernels.h"
+#include "norm.h"
 
 using namespace nvfp4moe;
 
@@ -381,6 +383,93 @@ struct Residual {
   const uint16_t* h;
   float a, b;
 };
+
+// ---------------------------------------------------------- 16-bit products ----
+constexpr int64_t kMaxElems = (int64_t)1 << 40;
+
+bool product_type(int32_t dtype) { return dtype == NVFP4MOE_BF16 || dtype == NVFP4MOE_FP16; }
+
+bool product_shape(int64_t M, int32_t K, int32_t N, int32_t E) {
+  if (M < 0 || M >= ((int64_t)1 << 30)) return false;
+  if (K < 8 || N < 8 || K % 8 != 0 || N % 8 != 0 || K > (1 << 19) || N > (1 << 19)) return false;
+  if (E < 1 || E > kMaxGroups) return false;
+  return M * (int64_t)(K > N ? K : N) < kMaxElems && (int64_t)K * N < kMaxElems / E;
+}
+
+struct ProductWs {
+  WsHeader* hdr;
+  int32_t* seg;
+  int32_t* tiles;
+  uint16_t* dz;            // linear_backward only
+  float* partials;
+  size_t bytes;
+};
+
+ProductWs carve_product(void* ws, int32_t E) {
+  Carver c(ws);
+  ProductWs p{};
+  p.hdr = c.take<WsHeader>(1);
+  p.seg = c.take<int32_t>(2 * (size_t)E);
+  p.tiles = c.take<int32_t>((size_t)E + 1);
+  p.bytes = c.off;
+  return p;
+}
+
+ProductWs carve_linear_backward(void* ws, int64_t M, int32_t N) {
+  Carver c(ws);
+  ProductWs p{};
+  p.hdr = c.take<WsHeader>(1);
+  p.dz = c.take<uint16_t>((size_t)(M * N));
+  p.partials = c.take<float>((size_t)act_grad_partials(M, N) * (size_t)N);
+  p.bytes = c.off;
+  return p;
+}
+
+// Resets the status word and builds the segment table of a ragged call (offsets != nullptr).
+cudaError_t start_product(const ProductWs& p, const int32_t* offsets, int E, int64_t M, cudaStream_t s) {
+  g_last_status = p.hdr;
+  const cudaError_t e = launch_mm_table(offsets, E, M, kMmTileRows, MmTable{p.seg, p.tiles}, &p.hdr->status, s);
+  if (e == cudaSuccess) ++g_launches;
+  return e;
+}
+
+MmArgs product_args(const ProductWs& p, bool ragged, int E, int64_t M, int32_t dtype) {
+  MmArgs m{};
+  m.seg = ragged ? p.seg : nullptr;
+  m.tiles = ragged ? p.tiles : nullptr;
+  m.E = E;
+  m.rows = M;
+  m.fp16 = dtype == NVFP4MOE_FP16;
+  m.status = &p.hdr->status;
+  return m;
+}
+
+// dx = dy W (per segment) and dw = dy^T x, either of them when asked for.
+cudaError_t product_gradients(const MmArgs& base, const void* dy, const void* x, const void* w, int32_t K, int32_t N,
+                              void* dx, void* dw, int32_t dw_dtype, cudaStream_t s) {
+  cudaError_t e = cudaSuccess;
+  if (dx != nullptr && base.rows > 0) {
+    MmArgs m = base;
+    m.J = K;
+    m.R = N;
+    m.out = dx;
+    e = launch_mm(kMmDgrad, dy, w, m, s);
+    if (e != cudaSuccess) return e;
+    ++g_launches;
+  }
+  if (dw != nullptr && base.rows == 0)
+    return cudaMemsetAsync(dw, 0, (size_t)base.E * N * K * (dw_dtype == NVFP4MOE_FP32 ? 4 : 2), s);
+  if (dw != nullptr) {
+    MmArgs m = base;
+    m.I = N;
+    m.J = K;
+    m.out = dw;
+    m.out_f32 = dw_dtype == NVFP4MOE_FP32;
+    e = launch_mm(kMmWgrad, dy, x, m, s);
+    if (e == cudaSuccess) ++g_launches;
+  }
+  return e;
+}
 
 struct StageEvents {
   void* const* ev;
@@ -1577,6 +1666,205 @@ int nvfp4moe_ep_combine(const float* rows, const int32_t* send_pos, int64_t T, i
     return cuda_failed();
   g_launches = 1;
   return NVFP4MOE_OK;
+}
+
+size_t nvfp4moe_grouped_mm_workspace_bytes(int32_t E) {
+  return E < 1 || E > kMaxGroups ? 0 : carve_product(nullptr, E).bytes;
+}
+
+int nvfp4moe_grouped_mm(int32_t dtype, const void* x, int64_t M, int32_t K, const void* w, int32_t E, int32_t N,
+                        const int32_t* offsets, void* y, void* ws, size_t ws_bytes, void* stream) {
+  g_launches = 0;
+  if (!product_type(dtype)) return NVFP4MOE_ERR_ARG;
+  if (!product_shape(M, K, N, E)) return NVFP4MOE_ERR_SHAPE;
+  if (w == nullptr || offsets == nullptr || ws == nullptr || (M > 0 && (x == nullptr || y == nullptr)))
+    return NVFP4MOE_ERR_ARG;
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, 16) || !aligned(offsets, 4) || !aligned(ws, kAlign))
+    return NVFP4MOE_ERR_ARG;
+  const ProductWs p = carve_product(ws, E);
+  if (ws_bytes < p.bytes) return NVFP4MOE_ERR_WORKSPACE;
+  const int st = check_device();
+  if (st != NVFP4MOE_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (start_product(p, offsets, E, M, s) != cudaSuccess) return cuda_failed();
+  if (M == 0) return NVFP4MOE_OK;
+  MmArgs m = product_args(p, true, E, M, dtype);
+  m.J = N;
+  m.R = K;
+  m.out = y;
+  if (launch_mm(kMmForward, x, w, m, s) != cudaSuccess) return cuda_failed();
+  ++g_launches;
+  return NVFP4MOE_OK;
+}
+
+int nvfp4moe_grouped_mm_backward(int32_t dtype, const void* dy, const void* x, const void* w, int64_t M, int32_t K,
+                                 int32_t E, int32_t N, const int32_t* offsets, void* dx, void* dw, int32_t dw_dtype,
+                                 void* ws, size_t ws_bytes, void* stream) {
+  g_launches = 0;
+  if (!product_type(dtype) || (dw != nullptr && dw_dtype != dtype && dw_dtype != NVFP4MOE_FP32)) return NVFP4MOE_ERR_ARG;
+  if (!product_shape(M, K, N, E)) return NVFP4MOE_ERR_SHAPE;
+  if ((dx == nullptr && dw == nullptr) || offsets == nullptr || ws == nullptr) return NVFP4MOE_ERR_ARG;
+  if (M > 0 && (dy == nullptr || (dw != nullptr && x == nullptr) || (dx != nullptr && w == nullptr)))
+    return NVFP4MOE_ERR_ARG;
+  if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(w, 16) || !aligned(dx, 16) || !aligned(dw, 16) ||
+      !aligned(offsets, 4) || !aligned(ws, kAlign))
+    return NVFP4MOE_ERR_ARG;
+  const ProductWs p = carve_product(ws, E);
+  if (ws_bytes < p.bytes) return NVFP4MOE_ERR_WORKSPACE;
+  const int st = check_device();
+  if (st != NVFP4MOE_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (start_product(p, offsets, E, M, s) != cudaSuccess) return cuda_failed();
+  if (product_gradients(product_args(p, true, E, M, dtype), dy, x, w, K, N, dx, dw, dw_dtype, s) != cudaSuccess)
+    return cuda_failed();
+  return NVFP4MOE_OK;
+}
+
+size_t nvfp4moe_linear_workspace_bytes(int64_t M, int32_t K, int32_t N) {
+  return product_shape(M, K, N, 1) ? carve_product(nullptr, 1).bytes : 0;
+}
+
+int nvfp4moe_linear(int32_t dtype, const void* x, int64_t M, int32_t K, const void* w, int32_t N, const float* bias,
+                    int32_t act, const void* residual, void* z_out, void* y, void* ws, size_t ws_bytes, void* stream) {
+  g_launches = 0;
+  if (!product_type(dtype) || act < NVFP4MOE_ACT_NONE || act > NVFP4MOE_ACT_GELU_TANH) return NVFP4MOE_ERR_ARG;
+  if (!product_shape(M, K, N, 1)) return NVFP4MOE_ERR_SHAPE;
+  if (w == nullptr || ws == nullptr || (M > 0 && (x == nullptr || y == nullptr))) return NVFP4MOE_ERR_ARG;
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, 16) || !aligned(bias, 16) || !aligned(residual, 16) ||
+      !aligned(z_out, 16) || !aligned(ws, kAlign))
+    return NVFP4MOE_ERR_ARG;
+  const ProductWs p = carve_product(ws, 1);
+  if (ws_bytes < p.bytes) return NVFP4MOE_ERR_WORKSPACE;
+  const int st = check_device();
+  if (st != NVFP4MOE_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (start_product(p, nullptr, 1, M, s) != cudaSuccess) return cuda_failed();
+  if (M == 0) return NVFP4MOE_OK;
+  MmArgs m = product_args(p, false, 1, M, dtype);
+  m.J = N;
+  m.R = K;
+  m.out = y;
+  m.bias = bias;
+  m.act = act;
+  m.residual = residual;
+  m.z_out = z_out;
+  if (launch_mm(kMmForward, x, w, m, s) != cudaSuccess) return cuda_failed();
+  ++g_launches;
+  return NVFP4MOE_OK;
+}
+
+size_t nvfp4moe_linear_backward_workspace_bytes(int64_t M, int32_t K, int32_t N) {
+  return product_shape(M, K, N, 1) ? carve_linear_backward(nullptr, M, N).bytes : 0;
+}
+
+int nvfp4moe_linear_backward(int32_t dtype, const void* dy, const void* x, const void* w, const void* z, int64_t M,
+                             int32_t K, int32_t N, int32_t act, void* dx, void* dw, int32_t dw_dtype, float* db,
+                             void* ws, size_t ws_bytes, void* stream) {
+  g_launches = 0;
+  if (!product_type(dtype) || act < NVFP4MOE_ACT_NONE || act > NVFP4MOE_ACT_GELU_TANH ||
+      (dw != nullptr && dw_dtype != dtype && dw_dtype != NVFP4MOE_FP32))
+    return NVFP4MOE_ERR_ARG;
+  if (!product_shape(M, K, N, 1)) return NVFP4MOE_ERR_SHAPE;
+  if ((dx == nullptr && dw == nullptr && db == nullptr) || ws == nullptr) return NVFP4MOE_ERR_ARG;
+  if (M > 0 && (dy == nullptr || (act != NVFP4MOE_ACT_NONE && z == nullptr) || (dw != nullptr && x == nullptr) ||
+                (dx != nullptr && w == nullptr)))
+    return NVFP4MOE_ERR_ARG;
+  if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(w, 16) || !aligned(z, 16) || !aligned(dx, 16) ||
+      !aligned(dw, 16) || !aligned(db, 4) || !aligned(ws, kAlign))
+    return NVFP4MOE_ERR_ARG;
+  const ProductWs p = carve_linear_backward(ws, M, N);
+  if (ws_bytes < p.bytes) return NVFP4MOE_ERR_WORKSPACE;
+  const int st = check_device();
+  if (st != NVFP4MOE_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (start_product(p, nullptr, 1, M, s) != cudaSuccess) return cuda_failed();
+  if (M == 0) {
+    if (db != nullptr && cudaMemsetAsync(db, 0, (size_t)N * sizeof(float), s) != cudaSuccess) return cuda_failed();
+  } else if (act != NVFP4MOE_ACT_NONE || db != nullptr) {
+    if (launch_act_grad(dy, z, M, N, act, dtype == NVFP4MOE_FP16, p.dz, db, p.partials, &g_launches, s) != cudaSuccess)
+      return cuda_failed();
+  }
+  const void* dz = act != NVFP4MOE_ACT_NONE ? p.dz : dy;
+  if (product_gradients(product_args(p, false, 1, M, dtype), dz, x, w, K, N, dx, dw, dw_dtype, s) != cudaSuccess)
+    return cuda_failed();
+  return NVFP4MOE_OK;
+}
+
+int nvfp4moe_layer_norm(int32_t dtype, const void* x, int64_t rows, int32_t cols, const float* gamma,
+                        const float* beta, float eps, int32_t rms, void* y, float* mean, float* rstd, void* stream) {
+  g_launches = 0;
+  if (dtype < NVFP4MOE_BF16 || dtype > NVFP4MOE_FP32 || !(eps >= 0.0f) || eps > 3.0e38f) return NVFP4MOE_ERR_ARG;
+  if (rows < 0 || rows >= ((int64_t)1 << 31) || cols < 1 || cols > kNormMaxCols) return NVFP4MOE_ERR_SHAPE;
+  if (rms != 0 && beta != nullptr) return NVFP4MOE_ERR_ARG;
+  if (rows > 0 && (x == nullptr || y == nullptr)) return NVFP4MOE_ERR_ARG;
+  if (!aligned(x, 16) || !aligned(y, 16) || !aligned(gamma, 4) || !aligned(beta, 4) || !aligned(mean, 4) ||
+      !aligned(rstd, 4))
+    return NVFP4MOE_ERR_ARG;
+  const int st = check_device();
+  if (st != NVFP4MOE_OK) return st;
+  if (rows == 0) return NVFP4MOE_OK;
+  NormArgs a{};
+  a.x = x;
+  a.gamma = gamma;
+  a.beta = beta;
+  a.mean = rms != 0 ? nullptr : mean;
+  a.rstd = rstd;
+  a.y = y;
+  a.rows = rows;
+  a.cols = cols;
+  a.eps = eps;
+  a.rms = rms != 0;
+  a.dtype = dtype;
+  return launch_norm_forward(a, &g_launches, static_cast<cudaStream_t>(stream)) == cudaSuccess ? NVFP4MOE_OK
+                                                                                               : cuda_failed();
+}
+
+size_t nvfp4moe_layer_norm_backward_workspace_bytes(int64_t rows, int32_t cols) {
+  if (rows < 0 || rows >= ((int64_t)1 << 31) || cols < 1 || cols > kNormMaxCols) return 0;
+  return align_up((size_t)(rows > 0 ? norm_backward_parts(rows, cols) : 1) * 2 * (size_t)cols * sizeof(float));
+}
+
+int nvfp4moe_layer_norm_backward(int32_t dtype, const void* dy, const void* x, int64_t rows, int32_t cols,
+                                 const float* gamma, const float* mean, const float* rstd, int32_t rms, void* dx,
+                                 float* dgamma, float* dbeta, void* ws, size_t ws_bytes, void* stream) {
+  g_launches = 0;
+  if (dtype < NVFP4MOE_BF16 || dtype > NVFP4MOE_FP32) return NVFP4MOE_ERR_ARG;
+  if (rows < 0 || rows >= ((int64_t)1 << 31) || cols < 1 || cols > kNormMaxCols) return NVFP4MOE_ERR_SHAPE;
+  if (rms != 0 && (dbeta != nullptr || mean != nullptr)) return NVFP4MOE_ERR_ARG;
+  if (rows > 0 && (dy == nullptr || x == nullptr || rstd == nullptr || dx == nullptr || (rms == 0 && mean == nullptr)))
+    return NVFP4MOE_ERR_ARG;
+  if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(dx, 16) || !aligned(gamma, 4) || !aligned(mean, 4) ||
+      !aligned(rstd, 4) || !aligned(dgamma, 4) || !aligned(dbeta, 4))
+    return NVFP4MOE_ERR_ARG;
+  const bool params = dgamma != nullptr || dbeta != nullptr;
+  if (params) {
+    if (ws == nullptr || !aligned(ws, kAlign)) return NVFP4MOE_ERR_ARG;
+    if (ws_bytes < nvfp4moe_layer_norm_backward_workspace_bytes(rows, cols)) return NVFP4MOE_ERR_WORKSPACE;
+  }
+  const int st = check_device();
+  if (st != NVFP4MOE_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (rows == 0) {
+    if ((dgamma != nullptr && cudaMemsetAsync(dgamma, 0, (size_t)cols * sizeof(float), s) != cudaSuccess) ||
+        (dbeta != nullptr && cudaMemsetAsync(dbeta, 0, (size_t)cols * sizeof(float), s) != cudaSuccess))
+      return cuda_failed();
+    return NVFP4MOE_OK;
+  }
+  NormArgs a{};
+  a.x = x;
+  a.gamma = gamma;
+  a.mean = const_cast<float*>(mean);
+  a.rstd = const_cast<float*>(rstd);
+  a.dy = dy;
+  a.dx = dx;
+  a.dgamma = dgamma;
+  a.dbeta = dbeta;
+  a.partials = params ? static_cast<float*>(ws) : nullptr;
+  a.rows = rows;
+  a.cols = cols;
+  a.rms = rms != 0;
+  a.dtype = dtype;
+  return launch_norm_backward(a, &g_launches, s) == cudaSuccess ? NVFP4MOE_OK : cuda_failed();
 }
 
 int32_t nvfp4moe_last_launch_count(void) { return g_launches; }

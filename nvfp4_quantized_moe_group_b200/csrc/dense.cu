@@ -1,0 +1,521 @@
+// 16-bit (BF16 / FP16) matrix products with FP32 accumulation on the 5th-generation tensor
+// cores: grouped by expert with ragged row segments, or dense with a bias, activation and
+// residual epilogue, and the products of their backward passes.
+//
+//   forward  y[i]  = x[i] W_e^T            dense: z = x W^T + b, y = act(z) + residual
+//   dgrad    dx[i] = dy[i] W_e
+//   wgrad    dW_e  = sum_i dy[i]^T x[i]    over the rows i of expert e's segment
+//
+// One kernel computes D[i][j] = sum_r A[i][r] B[j][r] for all three; an operand whose r runs
+// along memory is K-major in shared memory, one whose i or j does is MN-major (the transposed
+// read is the tensor core's: no operand is ever transposed in memory).
+//
+// A pair of CTAs (one on each SM of a TPC) computes a 256 x 256 tile: each loads its 128 rows of
+// A and its 128 rows of B (32 KB per 64-deep step, 6 stages), tcgen05.mma.cta_group::2 reads
+// both halves of B from both shared memories, and each CTA holds its 128 x 256 FP32 accumulator
+// in tensor memory, double buffered, so the epilogue of one tile overlaps the next one's MMAs.
+//
+// Per CTA: warp 0 loads (TMA, 128-byte swizzle); warp 2 passes each landed stage on to the pair's
+// issuing CTA (an arrival on its `ready` barrier), after zeroing what lies behind a ragged
+// segment's end: in wgrad the reduction runs over rows, and rows of the next segment (or rows
+// that were never written) would otherwise enter the sum, a NaN there even through a zero
+// factor, so both operands' rows are zeroed.  A row is a whole 128-byte line of the MN-major
+// tile, so the zeroed range is contiguous whatever the swizzle.  Warp 1 of the pair's first CTA
+// issues the MMAs; warps 4-7 run the epilogue through a padded shared-memory tile, so that global
+// accesses are whole 64-byte row pieces.  In forward and dgrad, rows behind a segment's end only
+// feed accumulator rows that are not stored.
+//
+// Every wait is bounded; one that runs out raises the timeout bit of the status word and the
+// pair winds down.
+#include "common.cuh"
+#include "dense.h"
+#include "dense_epilogue.cuh"
+#include "kernels.h"
+
+namespace nvfp4moe {
+
+namespace {
+
+constexpr int kBK = 64;                  // reduction values per stage (one 128-byte swizzle row)
+constexpr int kPairTile = 256;           // rows and columns of a pair's tile
+constexpr int kHalf = 128;               // each CTA's share of A rows and of B rows
+constexpr int kPairStages = 6;
+constexpr int kPairThreads = 256;
+constexpr int kOperandBytes = kHalf * kBK * 2;
+constexpr int kRasterRows = 16;          // row tiles that share a column tile before the next one
+
+// ------------------------------------------------------------- cluster helpers ----
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// Shared-memory address of this CTA -> the same address in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+
+__device__ __forceinline__ void mbar_arrive_rank(uint64_t* bar, uint32_t rank) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(map_rank(smem_u32(bar), rank))
+               : "memory");
+}
+
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// mbar_wait with cluster-scope acquire, ended early by the CTA's abort flag.
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, const int* abort_flag) {
+  if (mbar_try_wait_cluster(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  uint32_t n = 0;
+  while (!mbar_try_wait_cluster(bar, parity)) {
+    if ((++n & 63u) == 0u &&
+        (*reinterpret_cast<const volatile int*>(abort_flag) != 0 || globaltimer_ns() - t0 > kWaitLimitNs))
+      return false;
+  }
+  return true;
+}
+
+__device__ __forceinline__ void set_abort(int* flag, uint32_t* status) {
+  raise_status(status, kStatusTimeout);
+  *reinterpret_cast<volatile int*>(flag) = 1;
+}
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, uint64_t* bar, int32_t c0, int32_t c1,
+                                            int32_t c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(tmap), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+// ------------------------------------------------------------ tcgen05, CTA pairs ----
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+
+// Arrives on `bar` of both CTAs of the pair when this thread's tcgen05 operations so far are done.
+__device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
+__device__ __forceinline__ void mma_f16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// MN-major operand, 128-byte swizzle: 64 consecutive i (or j) per 128-byte line, one line per r;
+// 8 lines form a 1024-byte group, groups 1024 bytes apart along r; blocks of 64 i are
+// `block_bytes` apart.
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t block_bytes) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(block_bytes >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+// Instruction descriptor of kind::f16: FP32 accumulator, A and B of one 16-bit type, their
+// majorness, N / 8 at bit 17, M / 16 at bit 24.
+__host__ __device__ constexpr uint32_t idesc_f16(uint32_t m, uint32_t n, bool fp16, bool a_mn, bool b_mn) {
+  return (1u << 4) | ((fp16 ? 0u : 1u) << 7) | ((fp16 ? 0u : 1u) << 10) | ((a_mn ? 1u : 0u) << 15) |
+         ((b_mn ? 1u : 0u) << 16) | ((n >> 3) << 17) | ((m >> 4) << 24);
+}
+
+// --------------------------------------------------------------------- tiles ----
+struct Tile {
+  int e;
+  int a0, b0;        // kMmWgrad: first i, first j; else first token row, first j
+  int64_t out_row;   // row of D (in the whole output) that a0 is
+  int rows_valid;    // rows of the tile to store
+  int r0;            // kMmWgrad: first token row of the reduction
+  int steps;         // 64-deep reduction steps
+  int tail;          // valid values of the last step (kMmWgrad)
+};
+
+template <int kMode>
+__device__ __forceinline__ int total_tiles(const MmArgs& p, int tile_i, int tile_j) {
+  const int ntj = (p.J + tile_j - 1) / tile_j;
+  if constexpr (kMode == kMmWgrad) return p.E * ((p.I + tile_i - 1) / tile_i) * ntj;
+  return (p.tiles != nullptr ? p.tiles[p.E] : (int)((p.rows + tile_i - 1) / tile_i)) * ntj;
+}
+
+// Tile w in expert-major order; within an expert, blocks of kRasterRows row tiles go through the
+// column tiles together, row tile fastest (a column tile's weights are read by its row tiles at
+// about the same time, and a block's rows stay in L2 while it goes through the columns).
+template <int kMode>
+__device__ __forceinline__ Tile tile_at(const MmArgs& p, int w, int tile_i, int tile_j) {
+  Tile t;
+  const int ntj = (p.J + tile_j - 1) / tile_j;
+  int mt_e, local, seg_row = 0;
+  int64_t seg_rows = p.rows;
+  if constexpr (kMode == kMmWgrad) {
+    mt_e = (p.I + tile_i - 1) / tile_i;
+    t.e = w / (mt_e * ntj);
+    local = w - t.e * mt_e * ntj;
+  } else if (p.tiles != nullptr) {
+    int lo = 0, hi = p.E;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (p.tiles[mid] * ntj <= w) lo = mid; else hi = mid;
+    }
+    t.e = lo;
+    mt_e = p.tiles[lo + 1] - p.tiles[lo];
+    local = w - p.tiles[lo] * ntj;
+  } else {
+    t.e = 0;
+    mt_e = (int)((p.rows + tile_i - 1) / tile_i);
+    local = w;
+  }
+  if (p.seg != nullptr) {
+    seg_row = p.seg[2 * t.e];
+    seg_rows = p.seg[2 * t.e + 1];
+  }
+  const int block = local / (kRasterRows * ntj);
+  const int in_block = local - block * kRasterRows * ntj;
+  const int left_rows = mt_e - block * kRasterRows;
+  const int width = left_rows < kRasterRows ? left_rows : kRasterRows;
+  const int nt = in_block / width;
+  const int mt = block * kRasterRows + in_block - nt * width;
+  t.b0 = nt * tile_j;
+  if constexpr (kMode == kMmWgrad) {
+    t.a0 = mt * tile_i;
+    t.out_row = (int64_t)t.e * p.I + t.a0;
+    t.rows_valid = p.I - t.a0 < tile_i ? p.I - t.a0 : tile_i;
+    t.r0 = seg_row;
+    t.steps = (int)((seg_rows + kBK - 1) / kBK);
+    t.tail = (int)(seg_rows - (int64_t)(t.steps - 1) * kBK);
+  } else {
+    const int64_t left = seg_rows - (int64_t)mt * tile_i;
+    t.a0 = seg_row + mt * tile_i;
+    t.out_row = t.a0;
+    t.rows_valid = left < tile_i ? (int)left : tile_i;
+    t.r0 = 0;
+    t.steps = (p.R + kBK - 1) / kBK;
+    t.tail = kBK;
+  }
+  return t;
+}
+
+struct __align__(1024) PairSmem {
+  uint8_t a[kPairStages][kOperandBytes];
+  uint8_t b[kPairStages][kOperandBytes];
+  EpilogueTile epi[4];
+  uint64_t full[kPairStages];    // this CTA's loads of the stage have landed
+  uint64_t ready[kPairStages];   // (first CTA) both CTAs' stage may be read by the MMAs
+  uint64_t empty[kPairStages];   // the MMAs have read the stage
+  uint64_t acc_full[2];
+  uint64_t acc_empty[2];         // (first CTA) both CTAs' epilogues have read the accumulator
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+template <int kMode>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+               const __grid_constant__ MmArgs p) {
+  constexpr bool kAMn = kMode == kMmWgrad;
+  constexpr bool kBMn = kMode != kMmForward;
+  extern __shared__ uint8_t smem_raw[];
+  PairSmem& s = *reinterpret_cast<PairSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kPairStages; ++i) {
+      mbar_init(&s.full[i], 1);
+      mbar_init(&s.ready[i], 2);
+      mbar_init(&s.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.acc_full[i], 1);
+      mbar_init(&s.acc_empty[i], 8);
+    }
+    mbar_init(&s.drain, 1);
+    s.abort_flag = 0;
+    fence_barrier_init();
+    prefetch_tmap(&map_a);
+    prefetch_tmap(&map_b);
+  }
+  if (warp == 1) tmem_alloc_pair(&s.tmem_base, 512);
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  pdl_wait();
+  pdl_trigger();
+
+  const uint32_t tmem = s.tmem_base;
+  const int total = total_tiles<kMode>(p, kPairTile, kPairTile);
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------- loads ----
+    __syncwarp();
+    if (elect_one()) {
+      uint32_t stage = 0, phase = 0, issued = 0, issued_par = 0;
+      bool ok = true;
+      for (int w = pair; ok && w < total; w += pairs) {
+        const Tile t = tile_at<kMode>(p, w, kPairTile, kPairTile);
+        const int ai = t.a0 + (int)rank * kHalf, bj = t.b0 + (int)rank * kHalf;
+        for (int k = 0; k < t.steps; ++k) {
+          if (!wait_cluster(&s.empty[stage], phase ^ 1u, &s.abort_flag)) {
+            set_abort(&s.abort_flag, p.status);
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&s.full[stage], 2 * kOperandBytes);
+          const int r = t.r0 + k * kBK;
+          if constexpr (kAMn) {
+            tma_load_3d(s.a[stage], &map_a, &s.full[stage], ai, r, 0);
+            tma_load_3d(s.a[stage] + kOperandBytes / 2, &map_a, &s.full[stage], ai + 64, r, 0);
+          } else {
+            tma_load_3d(s.a[stage], &map_a, &s.full[stage], r, ai, 0);
+          }
+          if constexpr (kBMn) {
+            const int be = kMode == kMmWgrad ? 0 : t.e;
+            tma_load_3d(s.b[stage], &map_b, &s.full[stage], bj, r, be);
+            tma_load_3d(s.b[stage] + kOperandBytes / 2, &map_b, &s.full[stage], bj + 64, r, be);
+          } else {
+            tma_load_3d(s.b[stage], &map_b, &s.full[stage], r, bj, t.e);
+          }
+          issued |= 1u << stage;
+          issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+          if (++stage == kPairStages) { stage = 0; phase ^= 1u; }
+        }
+      }
+      // every copy this thread started has landed before the CTA can exit
+      for (int i = 0; i < kPairStages; ++i)
+        if ((issued >> i) & 1u)
+          if (!mbar_wait(&s.full[i], (issued_par >> i) & 1u)) set_abort(&s.abort_flag, p.status);
+    }
+  } else if (warp == 1) {
+    // --------------------------------------------------------------- MMAs ----
+    __syncwarp();
+    if (rank == 0 && elect_one()) {
+      uint32_t stage = 0, phase = 0;
+      const uint32_t idesc = idesc_f16(2 * kHalf, kPairTile, p.fp16 != 0, kAMn, kBMn);
+      bool ok = true;
+      int it = 0;
+      for (int w = pair; ok && w < total; w += pairs) {
+        const Tile t = tile_at<kMode>(p, w, kPairTile, kPairTile);
+        if (t.steps == 0) continue;
+        const uint32_t acc = tmem + (uint32_t)(it & 1) * kPairTile;
+        if (!wait_cluster(&s.acc_empty[it & 1], ((uint32_t)(it >> 1) & 1u) ^ 1u, &s.abort_flag)) {
+          set_abort(&s.abort_flag, p.status);
+          break;
+        }
+        tc_fence_after();
+        for (int k = 0; k < t.steps; ++k) {
+          if (!wait_cluster(&s.ready[stage], phase, &s.abort_flag)) {
+            set_abort(&s.abort_flag, p.status);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a0 = smem_u32(s.a[stage]), b0 = smem_u32(s.b[stage]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            // 16 values along r: 32 bytes of a K-major line, 16 lines of an MN-major tile
+            const uint64_t da = kAMn ? desc_mn_sw128(a0 + 2048 * j, kOperandBytes / 2) : desc_k_sw128(a0 + 32 * j);
+            const uint64_t db = kBMn ? desc_mn_sw128(b0 + 2048 * j, kOperandBytes / 2) : desc_k_sw128(b0 + 32 * j);
+            mma_f16_pair(acc, da, db, idesc, (k | j) != 0 ? 1u : 0u);
+          }
+          tc_commit_pair(&s.empty[stage]);
+          if (++stage == kPairStages) { stage = 0; phase ^= 1u; }
+        }
+        if (!ok) break;
+        tc_commit_pair(&s.acc_full[it & 1]);
+        ++it;
+      }
+      // every tensor-core operation of the pair is done before the memories are given back
+      tc_commit_pair(&s.drain);
+      if (!mbar_wait(&s.drain, 0)) set_abort(&s.abort_flag, p.status);
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------ stages passed on to the pair ----
+    uint32_t stage = 0, phase = 0;
+    bool ok = true;
+    for (int w = pair; ok && w < total; w += pairs) {
+      const Tile t = tile_at<kMode>(p, w, kPairTile, kPairTile);
+      for (int k = 0; k < t.steps; ++k) {
+        const bool got = wait_cluster(&s.full[stage], phase, &s.abort_flag);
+        if (__any_sync(0xffffffffu, !got)) {
+          set_abort(&s.abort_flag, p.status);
+          ok = false;
+          break;
+        }
+        if (kMode == kMmWgrad && k == t.steps - 1 && t.tail < kBK) {
+          // lines t.tail .. 63 of the four 64-line blocks
+          const int lines16 = (kBK - t.tail) * 8;
+          const uint4 zero = make_uint4(0, 0, 0, 0);
+          for (int i = lane; i < lines16; i += 32) {
+            uint8_t* at = s.a[stage] + t.tail * 128 + i * 16;
+            *reinterpret_cast<uint4*>(at) = zero;
+            *reinterpret_cast<uint4*>(at + kOperandBytes / 2) = zero;
+            at = s.b[stage] + t.tail * 128 + i * 16;
+            *reinterpret_cast<uint4*>(at) = zero;
+            *reinterpret_cast<uint4*>(at + kOperandBytes / 2) = zero;
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive_rank(&s.ready[stage], 0);
+        if (++stage == kPairStages) { stage = 0; phase ^= 1u; }
+      }
+    }
+  } else if (warp >= 4) {
+    // ----------------------------------------------------------- epilogue ----
+    const int q = warp & 3;
+    int it = 0;
+    for (int w = pair; w < total; w += pairs) {
+      const Tile t = tile_at<kMode>(p, w, kPairTile, kPairTile);
+      const int row0 = (int)rank * kHalf + q * 32;          // this warp's rows of the tile
+      const int live = t.rows_valid - row0;                 // of its 32 rows, those to store
+      const bool has_acc = t.steps > 0;
+      if (has_acc) {
+        const bool got = wait_cluster(&s.acc_full[it & 1], (uint32_t)(it >> 1) & 1u, &s.abort_flag);
+        if (__any_sync(0xffffffffu, !got)) {
+          set_abort(&s.abort_flag, p.status);
+          break;
+        }
+        tc_fence_after();
+      }
+      const uint32_t acc = tmem + (uint32_t)(it & 1) * kPairTile + ((uint32_t)(q * 32) << 16);
+      const int cols = p.J - t.b0 < kPairTile ? p.J - t.b0 : kPairTile;
+      if (live > 0) {
+        for (int c = 0; c < cols; c += 32) {
+          uint32_t v[32];
+          if (has_acc) {
+            tmem_ld_32x32b_x32(acc + c, v);
+            tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0u;
+          }
+          store_rows32(s.epi[q], v, p, t.out_row + row0, live, t.b0 + c, lane);
+        }
+      }
+      if (has_acc) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_rank(&s.acc_empty[it & 1], 0);
+        ++it;
+      }
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+
+// One thread per expert: its segment from the offsets, and the scan of the row tiles.
+__global__ void __launch_bounds__(kMaxGroups) mm_table_kernel(const int32_t* offsets, int E, int64_t rows,
+                                                              int tile_rows, MmTable t, uint32_t* status) {
+  __shared__ int warp_sum[32];
+  pdl_wait();
+  pdl_trigger();
+  const int e = threadIdx.x, lane = e & 31, warp = e >> 5;
+  int64_t lo = 0, hi = 0;
+  if (offsets != nullptr && e < E) {
+    lo = offsets[e];
+    hi = offsets[e + 1];
+  }
+  const bool bad = __syncthreads_or(lo < 0 || hi < lo || hi > rows);
+  if (e == 0) *status = bad ? kStatusBadInput : 0u;
+  if (offsets == nullptr) return;
+  if (bad) lo = hi = 0;
+  const int n = (int)((hi - lo + tile_rows - 1) / tile_rows);
+  int sum = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += up;
+  }
+  if (lane == 31) warp_sum[warp] = sum;
+  __syncthreads();
+  int before = 0;
+  for (int i = 0; i < warp; ++i) before += warp_sum[i];
+  if (e < E) {
+    t.seg[2 * e] = (int)lo;
+    t.seg[2 * e + 1] = (int)(hi - lo);
+    t.tiles[e + 1] = before + sum;
+  }
+  if (e == 0) t.tiles[0] = 0;
+}
+
+template <int kMode>
+cudaError_t launch_pair(const void* a, const void* b, const MmArgs& m, cudaStream_t stream) {
+  CUtensorMap map_a, map_b;
+  int err;
+  if (kMode == kMmWgrad) {
+    err = make_tma_16(&map_a, a, m.I, m.rows, 1, kBK) | make_tma_16(&map_b, b, m.J, m.rows, 1, kBK);
+  } else {
+    err = make_tma_16(&map_a, a, m.R, m.rows, 1, kHalf);
+    err |= kMode == kMmForward ? make_tma_16(&map_b, b, m.R, m.J, m.E, kHalf)
+                               : make_tma_16(&map_b, b, m.J, m.R, m.E, kBK);
+  }
+  if (err != 0) return cudaErrorInvalidValue;
+  const size_t smem = sizeof(PairSmem) + 1024;
+  static_assert(sizeof(PairSmem) + 1024 <= 232448, "shared memory exceeds the per-block limit");
+  cudaError_t ce = cudaFuncSetAttribute(mm_pair_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (ce != cudaSuccess) return ce;
+  const int64_t ntj = (m.J + kPairTile - 1) / kPairTile;
+  int64_t most = kMode == kMmWgrad ? (int64_t)m.E * ((m.I + kPairTile - 1) / kPairTile)
+                                   : (m.rows + kPairTile - 1) / kPairTile + (m.seg != nullptr ? m.E : 0);
+  most *= ntj;
+  const int64_t pairs = num_sms() / 2;
+  return launch_pdl(mm_pair_kernel<kMode>, dim3((unsigned)(2 * (most < pairs ? most : pairs))), dim3(kPairThreads),
+                    smem, stream, map_a, map_b, m);
+}
+
+}  // namespace
+
+cudaError_t launch_mm_table(const int32_t* offsets, int E, int64_t rows, int tile_rows, const MmTable& t,
+                            uint32_t* status, cudaStream_t stream) {
+  const int threads = offsets == nullptr ? 32 : (E + 31) / 32 * 32;
+  return launch_pdl(mm_table_kernel, dim3(1), dim3(threads), 0, stream, offsets, E, rows, tile_rows, t, status);
+}
+
+cudaError_t launch_mm(int mode, const void* a, const void* b, const MmArgs& m, cudaStream_t stream) {
+  switch (mode) {
+    case kMmForward: return launch_pair<kMmForward>(a, b, m, stream);
+    case kMmDgrad: return launch_pair<kMmDgrad>(a, b, m, stream);
+    default: return launch_pair<kMmWgrad>(a, b, m, stream);
+  }
+}
+
+}  // namespace nvfp4moe

@@ -1,0 +1,65 @@
+// Interface of the 16-bit products (dense.cu): grouped by expert or dense, with their gradients.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+namespace nvfp4moe {
+
+constexpr int kMmTileRows = 256;       // token rows of a tile (forward, dgrad)
+constexpr int kMaxGroups = 1024;       // experts of one grouped product (one thread each in the table kernel)
+
+// D[i][j] = sum_r A[i][r] B[j][r], per segment (expert) e:
+//   kMmForward  i: token rows of the segment, j: output features, r: input features
+//               A = x [rows][R], B = w [E][J][R]
+//   kMmDgrad    i: token rows, j: input features, r: output features
+//               A = dy [rows][R], B = w [E][R][J]
+//   kMmWgrad    i: output features, j: input features, r: token rows of the segment
+//               A = dy [rows][I], B = x [rows][J], D = dw [E][I][J]
+enum : int { kMmForward = 0, kMmDgrad = 1, kMmWgrad = 2 };
+
+// The segments of a ragged call, written by launch_mm_table into the workspace.
+struct MmTable {
+  int32_t* seg;          // [E][2] first row, number of rows
+  int32_t* tiles;        // [E + 1] row tiles before each segment
+};
+
+struct MmArgs {
+  const int32_t* seg;    // as in MmTable; nullptr: one segment, all `rows` rows
+  const int32_t* tiles;
+  int E;
+  int64_t rows;          // token rows of the tensors
+  int I;                 // kMmWgrad: rows of one expert's output
+  int J;                 // output columns
+  int R;                 // reduction length (not kMmWgrad)
+  int fp16;              // operands FP16 (else BF16)
+  void* out;
+  int out_f32;           // out is FP32 (else the operands' type)
+  const float* bias;     // [J] or nullptr
+  int act;               // NVFP4MOE_ACT_*
+  const void* residual;  // [rows][J] or nullptr, the operands' type
+  void* z_out;           // [rows][J] or nullptr: the sums with the bias, before the activation
+  uint32_t* status;
+};
+
+// Zeroes the status word and, with offsets, checks them and writes the segment table for row
+// tiles of tile_rows.  Offsets that decrease or leave 0 .. rows raise kStatusBadInput and leave
+// every segment empty, so no later kernel of the call reads or writes through them.
+cudaError_t launch_mm_table(const int32_t* offsets, int E, int64_t rows, int tile_rows, const MmTable& t,
+                            uint32_t* status, cudaStream_t stream);
+// The product.  a, b: the operands' base addresses.
+cudaError_t launch_mm(int mode, const void* a, const void* b, const MmArgs& m, cudaStream_t stream);
+
+// dz = dy act'(z) (16 bit, written when act is not NONE) and db[n] = sum_m dy act'(z) (FP32, when
+// db is not nullptr; partials: act_grad_partials(M) * N floats).
+int act_grad_partials(int64_t M, int64_t N);
+cudaError_t launch_act_grad(const void* dy, const void* z, int64_t M, int N, int act, bool fp16, void* dz, float* db,
+                            float* partials, int* launches, cudaStream_t stream);
+
+// gemm.cu: tensor map of 16-bit elements [batch][rows][inner], a 64 x box_rows x 1 box, 128B swizzle.
+int make_tma_16(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint64_t batch,
+                uint32_t box_rows);
+
+}  // namespace nvfp4moe

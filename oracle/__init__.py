@@ -47,4 +47,4 @@ from .router import route, RouteResult  # noqa: F401
 from .moe import permutation, expert_mlp, moe_forward, QuantTensor, quantize_tensor  # noqa: F401
 from .residual import rmsnorm, rmsnorm_scale, residual_weights, residual_add  # noqa: F401
 from .local_hessian import quantize_local_hessian, hessian_blocks, candidate_offsets  # noqa: F401
-from . import fp8  # noqa: F401
+from . import fp8, dense  # noqa: F401
