@@ -15,15 +15,18 @@
 // both halves of B from both shared memories, and each CTA holds its 128 x 256 FP32 accumulator
 // in tensor memory, double buffered, so the epilogue of one tile overlaps the next one's MMAs.
 //
-// Per CTA: warp 0 loads (TMA, 128-byte swizzle); warp 2 passes each landed stage on to the pair's
-// issuing CTA (an arrival on its `ready` barrier), after zeroing what lies behind a ragged
-// segment's end: in wgrad the reduction runs over rows, and rows of the next segment (or rows
-// that were never written) would otherwise enter the sum, a NaN there even through a zero
-// factor, so both operands' rows are zeroed.  A row is a whole 128-byte line of the MN-major
-// tile, so the zeroed range is contiguous whatever the swizzle.  Warp 1 of the pair's first CTA
-// issues the MMAs; warps 4-7 run the epilogue through a padded shared-memory tile, so that global
-// accesses are whole 64-byte row pieces.  In forward and dgrad, rows behind a segment's end only
-// feed accumulator rows that are not stored.
+// Per CTA: warp 0 loads (TMA, 128-byte swizzle), both CTAs' bytes counted on the first CTA's
+// barrier; warp 1 of the first CTA issues the MMAs; warps 4-7 run the epilogue through a padded
+// shared-memory tile, so that global accesses are whole 64-byte row pieces.
+//
+// Ragged ends.  In forward and dgrad, rows behind a segment's end only feed accumulator rows that
+// are not stored.  In wgrad the reduction runs over rows, so the last step of a segment would add
+// rows of the next one (or rows never written, where a NaN passes even a zero factor): warp 2 of
+// each CTA zeroes the lines behind the end in both operands before that step's MMAs.  A row is a
+// whole 128-byte line of the MN-major tile, so the range is contiguous whatever the swizzle.  Only
+// such a step takes the extra hop (its own barriers); passing every stage through a
+// release.cluster arrival cost a fence's latency per stage (4096 x 5120 x 5120: 388 us, 150 us
+// without).
 //
 // Every wait is bounded; one that runs out raises the timeout bit of the status word and the
 // pair winds down.
@@ -62,7 +65,12 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
   return r;
 }
 
+// Arrival on CTA `rank`'s barrier; the release form also makes this thread's earlier
+// shared-memory writes visible across the cluster.
 __device__ __forceinline__ void mbar_arrive_rank(uint64_t* bar, uint32_t rank) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(map_rank(smem_u32(bar), rank)) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_rank_release(uint64_t* bar, uint32_t rank) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(map_rank(smem_u32(bar), rank))
                : "memory");
 }
@@ -97,12 +105,14 @@ __device__ __forceinline__ void set_abort(int* flag, uint32_t* status) {
   *reinterpret_cast<volatile int*>(flag) = 1;
 }
 
-__device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, uint64_t* bar, int32_t c0, int32_t c1,
-                                            int32_t c2) {
+// Tiled load into this CTA's shared memory, completion counted on a barrier of either CTA of the
+// pair (bar: a shared::cluster address).
+__device__ __forceinline__ void tma_load_pair(void* dst, const void* tmap, uint32_t bar, int32_t c0, int32_t c1,
+                                              int32_t c2) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(tmap), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      "l"(tmap), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
       : "memory");
 }
 
@@ -229,8 +239,9 @@ struct __align__(1024) PairSmem {
   uint8_t a[kPairStages][kOperandBytes];
   uint8_t b[kPairStages][kOperandBytes];
   EpilogueTile epi[4];
-  uint64_t full[kPairStages];    // this CTA's loads of the stage have landed
-  uint64_t ready[kPairStages];   // (first CTA) both CTAs' stage may be read by the MMAs
+  uint64_t full[kPairStages];        // (first CTA) both CTAs' loads of the stage have landed
+  uint64_t tail_full[kPairStages];   // this CTA's loads of a ragged last step have landed
+  uint64_t tail_ready[kPairStages];  // (first CTA) both CTAs have zeroed the rows behind it
   uint64_t empty[kPairStages];   // the MMAs have read the stage
   uint64_t acc_full[2];
   uint64_t acc_empty[2];         // (first CTA) both CTAs' epilogues have read the accumulator
@@ -255,7 +266,8 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
   if (threadIdx.x == 0) {
     for (int i = 0; i < kPairStages; ++i) {
       mbar_init(&s.full[i], 1);
-      mbar_init(&s.ready[i], 2);
+      mbar_init(&s.tail_full[i], 1);
+      mbar_init(&s.tail_ready[i], 2);
       mbar_init(&s.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -283,7 +295,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     // ------------------------------------------------------------- loads ----
     __syncwarp();
     if (elect_one()) {
-      uint32_t stage = 0, phase = 0, issued = 0, issued_par = 0;
+      uint32_t stage = 0, phase = 0;
       bool ok = true;
       for (int w = pair; ok && w < total; w += pairs) {
         const Tile t = tile_at<kMode>(p, w, kPairTile, kPairTile);
@@ -294,36 +306,43 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&s.full[stage], 2 * kOperandBytes);
+          uint32_t bar = map_rank(smem_u32(&s.full[stage]), 0);
+          if (kMode == kMmWgrad && k == t.steps - 1 && t.tail < kBK) {
+            if (rank == 0) mbar_arrive(&s.full[stage]);
+            mbar_arrive_expect_tx(&s.tail_full[stage], 2 * kOperandBytes);
+            bar = smem_u32(&s.tail_full[stage]);
+          } else if (rank == 0) {
+            mbar_arrive_expect_tx(&s.full[stage], 4 * kOperandBytes);
+          }
           const int r = t.r0 + k * kBK;
           if constexpr (kAMn) {
-            tma_load_3d(s.a[stage], &map_a, &s.full[stage], ai, r, 0);
-            tma_load_3d(s.a[stage] + kOperandBytes / 2, &map_a, &s.full[stage], ai + 64, r, 0);
+            tma_load_pair(s.a[stage], &map_a, bar, ai, r, 0);
+            tma_load_pair(s.a[stage] + kOperandBytes / 2, &map_a, bar, ai + 64, r, 0);
           } else {
-            tma_load_3d(s.a[stage], &map_a, &s.full[stage], r, ai, 0);
+            tma_load_pair(s.a[stage], &map_a, bar, r, ai, 0);
           }
           if constexpr (kBMn) {
             const int be = kMode == kMmWgrad ? 0 : t.e;
-            tma_load_3d(s.b[stage], &map_b, &s.full[stage], bj, r, be);
-            tma_load_3d(s.b[stage] + kOperandBytes / 2, &map_b, &s.full[stage], bj + 64, r, be);
+            tma_load_pair(s.b[stage], &map_b, bar, bj, r, be);
+            tma_load_pair(s.b[stage] + kOperandBytes / 2, &map_b, bar, bj + 64, r, be);
           } else {
-            tma_load_3d(s.b[stage], &map_b, &s.full[stage], r, bj, t.e);
+            tma_load_pair(s.b[stage], &map_b, bar, r, bj, t.e);
           }
-          issued |= 1u << stage;
-          issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
           if (++stage == kPairStages) { stage = 0; phase ^= 1u; }
         }
       }
-      // every copy this thread started has landed before the CTA can exit
-      for (int i = 0; i < kPairStages; ++i)
-        if ((issued >> i) & 1u)
-          if (!mbar_wait(&s.full[i], (issued_par >> i) & 1u)) set_abort(&s.abort_flag, p.status);
+      // Every copy has landed once the pair's last MMAs have read it, which the cluster barrier at
+      // the end waits for.  A pair that gives up has none: its copies get a millisecond to land.
+      if (!ok) {
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(10000);
+      }
     }
   } else if (warp == 1) {
     // --------------------------------------------------------------- MMAs ----
     __syncwarp();
     if (rank == 0 && elect_one()) {
-      uint32_t stage = 0, phase = 0;
+      uint32_t stage = 0, phase = 0, tail_par = 0;
       const uint32_t idesc = idesc_f16(2 * kHalf, kPairTile, p.fp16 != 0, kAMn, kBMn);
       bool ok = true;
       int it = 0;
@@ -337,7 +356,12 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         }
         tc_fence_after();
         for (int k = 0; k < t.steps; ++k) {
-          if (!wait_cluster(&s.ready[stage], phase, &s.abort_flag)) {
+          bool landed = wait_cluster(&s.full[stage], phase, &s.abort_flag);
+          if (kMode == kMmWgrad && k == t.steps - 1 && t.tail < kBK) {
+            landed = landed && wait_cluster(&s.tail_ready[stage], (tail_par >> stage) & 1u, &s.abort_flag);
+            tail_par ^= 1u << stage;
+          }
+          if (!landed) {
             set_abort(&s.abort_flag, p.status);
             ok = false;
             break;
@@ -362,37 +386,35 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
       tc_commit_pair(&s.drain);
       if (!mbar_wait(&s.drain, 0)) set_abort(&s.abort_flag, p.status);
     }
-  } else if (warp == 2) {
-    // ------------------------------------------ stages passed on to the pair ----
-    uint32_t stage = 0, phase = 0;
-    bool ok = true;
-    for (int w = pair; ok && w < total; w += pairs) {
+  } else if (kMode == kMmWgrad && warp == 2) {
+    // ------------------------------------------- rows behind a segment's end ----
+    uint32_t stage = 0, tail_par = 0;
+    for (int w = pair; w < total; w += pairs) {
       const Tile t = tile_at<kMode>(p, w, kPairTile, kPairTile);
-      for (int k = 0; k < t.steps; ++k) {
-        const bool got = wait_cluster(&s.full[stage], phase, &s.abort_flag);
-        if (__any_sync(0xffffffffu, !got)) {
-          set_abort(&s.abort_flag, p.status);
-          ok = false;
-          break;
-        }
-        if (kMode == kMmWgrad && k == t.steps - 1 && t.tail < kBK) {
-          // lines t.tail .. 63 of the four 64-line blocks
-          const int lines16 = (kBK - t.tail) * 8;
-          const uint4 zero = make_uint4(0, 0, 0, 0);
-          for (int i = lane; i < lines16; i += 32) {
-            uint8_t* at = s.a[stage] + t.tail * 128 + i * 16;
-            *reinterpret_cast<uint4*>(at) = zero;
-            *reinterpret_cast<uint4*>(at + kOperandBytes / 2) = zero;
-            at = s.b[stage] + t.tail * 128 + i * 16;
-            *reinterpret_cast<uint4*>(at) = zero;
-            *reinterpret_cast<uint4*>(at + kOperandBytes / 2) = zero;
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive_rank(&s.ready[stage], 0);
-        if (++stage == kPairStages) { stage = 0; phase ^= 1u; }
+      if (t.steps == 0) continue;
+      const uint32_t at = (stage + (uint32_t)t.steps - 1) % kPairStages;     // the last step's stage
+      stage = (stage + (uint32_t)t.steps) % kPairStages;
+      if (t.tail == kBK) continue;
+      const bool got = wait_cluster(&s.tail_full[at], (tail_par >> at) & 1u, &s.abort_flag);
+      tail_par ^= 1u << at;
+      if (__any_sync(0xffffffffu, !got)) {
+        set_abort(&s.abort_flag, p.status);
+        break;
       }
+      // lines t.tail .. 63 of the four 64-line blocks
+      const int lines16 = (kBK - t.tail) * 8;
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+      for (int i = lane; i < lines16; i += 32) {
+        uint8_t* dst = s.a[at] + t.tail * 128 + i * 16;
+        *reinterpret_cast<uint4*>(dst) = zero;
+        *reinterpret_cast<uint4*>(dst + kOperandBytes / 2) = zero;
+        dst = s.b[at] + t.tail * 128 + i * 16;
+        *reinterpret_cast<uint4*>(dst) = zero;
+        *reinterpret_cast<uint4*>(dst + kOperandBytes / 2) = zero;
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive_rank_release(&s.tail_ready[at], 0);
     }
   } else if (warp >= 4) {
     // ----------------------------------------------------------- epilogue ----
