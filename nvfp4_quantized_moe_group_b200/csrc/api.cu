@@ -426,9 +426,11 @@ ProductWs carve_linear_backward(void* ws, int64_t M, int32_t N) {
 }
 
 // Resets the status word and builds the segment table of a ragged call (offsets != nullptr).
-cudaError_t start_product(const ProductWs& p, const int32_t* offsets, int E, int64_t M, cudaStream_t s) {
+// J, R: the columns and reduction length of the call's row product (forward or dgrad).
+cudaError_t start_product(const ProductWs& p, const int32_t* offsets, int E, int64_t M, int J, int R, cudaStream_t s) {
   g_last_status = p.hdr;
-  const cudaError_t e = launch_mm_table(offsets, E, M, kMmTileRows, MmTable{p.seg, p.tiles}, &p.hdr->status, s);
+  const int tile_rows = mm_plan(M, E, J, R, offsets != nullptr).tile_rows;
+  const cudaError_t e = launch_mm_table(offsets, E, M, tile_rows, MmTable{p.seg, p.tiles}, &p.hdr->status, s);
   if (e == cudaSuccess) ++g_launches;
   return e;
 }
@@ -1686,7 +1688,7 @@ int nvfp4moe_grouped_mm(int32_t dtype, const void* x, int64_t M, int32_t K, cons
   const int st = check_device();
   if (st != NVFP4MOE_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (start_product(p, offsets, E, M, s) != cudaSuccess) return cuda_failed();
+  if (start_product(p, offsets, E, M, N, K, s) != cudaSuccess) return cuda_failed();
   if (M == 0) return NVFP4MOE_OK;
   MmArgs m = product_args(p, true, E, M, dtype);
   m.J = N;
@@ -1714,7 +1716,7 @@ int nvfp4moe_grouped_mm_backward(int32_t dtype, const void* dy, const void* x, c
   const int st = check_device();
   if (st != NVFP4MOE_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (start_product(p, offsets, E, M, s) != cudaSuccess) return cuda_failed();
+  if (start_product(p, offsets, E, M, K, N, s) != cudaSuccess) return cuda_failed();
   if (product_gradients(product_args(p, true, E, M, dtype), dy, x, w, K, N, dx, dw, dw_dtype, s) != cudaSuccess)
     return cuda_failed();
   return NVFP4MOE_OK;
@@ -1738,7 +1740,7 @@ int nvfp4moe_linear(int32_t dtype, const void* x, int64_t M, int32_t K, const vo
   const int st = check_device();
   if (st != NVFP4MOE_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (start_product(p, nullptr, 1, M, s) != cudaSuccess) return cuda_failed();
+  if (start_product(p, nullptr, 1, M, N, K, s) != cudaSuccess) return cuda_failed();
   if (M == 0) return NVFP4MOE_OK;
   MmArgs m = product_args(p, false, 1, M, dtype);
   m.J = N;
@@ -1777,7 +1779,7 @@ int nvfp4moe_linear_backward(int32_t dtype, const void* dy, const void* x, const
   const int st = check_device();
   if (st != NVFP4MOE_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (start_product(p, nullptr, 1, M, s) != cudaSuccess) return cuda_failed();
+  if (start_product(p, nullptr, 1, M, N, K, s) != cudaSuccess) return cuda_failed();
   if (M == 0) {
     if (db != nullptr && cudaMemsetAsync(db, 0, (size_t)N * sizeof(float), s) != cudaSuccess) return cuda_failed();
   } else if (act != NVFP4MOE_ACT_NONE || db != nullptr) {

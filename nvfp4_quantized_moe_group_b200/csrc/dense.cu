@@ -464,6 +464,258 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
 
+// ------------------------------------------------------------- few rows ----
+// Products with few token rows per segment (decode, small experts) read the weights once and little
+// else, so the weights are the 128-row operand and the tokens the narrow one: a tile is 128 output
+// columns x kTok token rows, D^T[j][i] = sum_r W[j][r] x[i][r], on one CTA (cta_group::1).  16 KB of
+// weights arrive per 64-deep step through a deep ring, which keeps enough loads in flight for
+// HBM; padding the tokens to kTok costs tensor time only.  When there are fewer tiles than SMs, a
+// cluster of `split` CTAs shares a tile's reduction: each adds its part of the steps, the parts meet
+// in distributed shared memory and each CTA sums and stores some of the token rows, in rank order
+// (a fixed order of additions, no workspace).
+constexpr int kNarrowThreads = 256;
+constexpr int kMaxSplit = 8;
+
+template <int kTok>
+struct NarrowCfg {
+  static constexpr int kStages = kTok <= 16 ? 10 : kTok <= 32 ? 9 : kTok <= 64 ? 7 : 5;
+  static constexpr uint32_t kAccCols = kTok < 16 ? 16 : kTok;
+  static constexpr uint32_t kTmemCols = 2 * kAccCols < 32 ? 32 : 2 * kAccCols;
+};
+
+template <int kTok>
+struct __align__(1024) NarrowSmem {
+  uint8_t w[NarrowCfg<kTok>::kStages][kOperandBytes];
+  uint8_t x[NarrowCfg<kTok>::kStages][kTok * kBK * 2];
+  float part[kTok][kHalf];            // this CTA's sums of the tile, token-major
+  uint64_t full[NarrowCfg<kTok>::kStages];
+  uint64_t empty[NarrowCfg<kTok>::kStages];
+  uint64_t acc_full[2];
+  uint64_t acc_empty[2];
+  uint64_t part_full;                 // every CTA of the cluster has written its part
+  uint64_t part_empty;                // every CTA has read this CTA's part
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+__device__ __forceinline__ void tma_load_cta(void* dst, const void* tmap, uint64_t* bar, int32_t c0, int32_t c1,
+                                             int32_t c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(tmap), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+__device__ __forceinline__ void mma_f16_cta(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+template <int kMode, int kTok>
+__global__ void __launch_bounds__(kNarrowThreads, 1)
+mm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                 const __grid_constant__ MmArgs p, int split) {
+  using C = NarrowCfg<kTok>;
+  constexpr int kStages = C::kStages;
+  constexpr bool kWMn = kMode == kMmDgrad;
+  constexpr int kXBytes = kTok * kBK * 2;
+  extern __shared__ uint8_t smem_raw[];
+  NarrowSmem<kTok>& s = *reinterpret_cast<NarrowSmem<kTok>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                             ~static_cast<uintptr_t>(1023));
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int rank = split > 1 ? (int)cluster_rank() : 0;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&s.full[i], 1);
+      mbar_init(&s.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.acc_full[i], 1);
+      mbar_init(&s.acc_empty[i], 4);
+    }
+    mbar_init(&s.part_full, 4 * split);
+    mbar_init(&s.part_empty, 4 * split);
+    mbar_init(&s.drain, 1);
+    s.abort_flag = 0;
+    fence_barrier_init();
+    prefetch_tmap(&map_w);
+    prefetch_tmap(&map_x);
+  }
+  if (warp == 1) {
+    tmem_alloc(&s.tmem_base, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  if (split > 1) cluster_sync(); else __syncthreads();
+  tc_fence_after();
+  pdl_wait();
+  pdl_trigger();
+
+  const uint32_t tmem = s.tmem_base;
+  const int total = total_tiles<kMode>(p, kTok, kHalf);
+  const int first = blockIdx.x / split, step = gridDim.x / split;
+  const int all_steps = (p.R + kBK - 1) / kBK;
+  // this CTA's part of every tile's reduction (at least one step: split <= all_steps)
+  const int k0 = (int)((int64_t)all_steps * rank / split), k1 = (int)((int64_t)all_steps * (rank + 1) / split);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------- loads ----
+    __syncwarp();
+    if (elect_one()) {
+      uint32_t stage = 0, phase = 0, issued = 0, issued_par = 0;
+      bool ok = true;
+      for (int w = first; ok && w < total; w += step) {
+        const Tile t = tile_at<kMode>(p, w, kTok, kHalf);
+        for (int k = k0; k < k1; ++k) {
+          if (!wait_cluster(&s.empty[stage], phase ^ 1u, &s.abort_flag)) {
+            set_abort(&s.abort_flag, p.status);
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&s.full[stage], kOperandBytes + kXBytes);
+          const int r = k * kBK;
+          if constexpr (kWMn) {
+            tma_load_cta(s.w[stage], &map_w, &s.full[stage], t.b0, r, t.e);
+            tma_load_cta(s.w[stage] + kOperandBytes / 2, &map_w, &s.full[stage], t.b0 + 64, r, t.e);
+          } else {
+            tma_load_cta(s.w[stage], &map_w, &s.full[stage], r, t.b0, t.e);
+          }
+          tma_load_cta(s.x[stage], &map_x, &s.full[stage], r, t.a0, 0);
+          issued |= 1u << stage;
+          issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+          if (++stage == kStages) { stage = 0; phase ^= 1u; }
+        }
+      }
+      // every copy this thread started has landed before the CTA can exit
+      for (int i = 0; i < kStages; ++i)
+        if ((issued >> i) & 1u)
+          if (!mbar_wait(&s.full[i], (issued_par >> i) & 1u)) set_abort(&s.abort_flag, p.status);
+    }
+  } else if (warp == 1) {
+    // --------------------------------------------------------------- MMAs ----
+    __syncwarp();
+    if (elect_one()) {
+      uint32_t stage = 0, phase = 0;
+      const uint32_t idesc = idesc_f16(kHalf, kTok, p.fp16 != 0, kWMn, false);
+      bool ok = true;
+      int it = 0;
+      for (int w = first; ok && w < total; w += step, ++it) {
+        const uint32_t acc = tmem + (uint32_t)(it & 1) * C::kAccCols;
+        if (!wait_cluster(&s.acc_empty[it & 1], ((uint32_t)(it >> 1) & 1u) ^ 1u, &s.abort_flag)) {
+          set_abort(&s.abort_flag, p.status);
+          break;
+        }
+        tc_fence_after();
+        for (int k = k0; k < k1; ++k) {
+          if (!wait_cluster(&s.full[stage], phase, &s.abort_flag)) {
+            set_abort(&s.abort_flag, p.status);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t w0 = smem_u32(s.w[stage]), x0 = smem_u32(s.x[stage]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint64_t dw = kWMn ? desc_mn_sw128(w0 + 2048 * j, kOperandBytes / 2) : desc_k_sw128(w0 + 32 * j);
+            mma_f16_cta(acc, dw, desc_k_sw128(x0 + 32 * j), idesc, k != k0 || j != 0 ? 1u : 0u);
+          }
+          tc_commit(&s.empty[stage]);
+          if (++stage == kStages) { stage = 0; phase ^= 1u; }
+        }
+        if (!ok) break;
+        tc_commit(&s.acc_full[it & 1]);
+      }
+      // every tensor-core operation is done before the memories are given back
+      tc_commit(&s.drain);
+      if (!mbar_wait(&s.drain, 0)) set_abort(&s.abort_flag, p.status);
+    }
+  } else if (warp >= 4) {
+    // ----------------------------------------------------------- epilogue ----
+    const int q = warp & 3;
+    int it = 0;
+    for (int w = first; w < total; w += step, ++it) {
+      const Tile t = tile_at<kMode>(p, w, kTok, kHalf);
+      bool got = wait_cluster(&s.acc_full[it & 1], (uint32_t)(it >> 1) & 1u, &s.abort_flag);
+      // the tile before this one has been read by every CTA of the cluster
+      if (it > 0) got = got && wait_cluster(&s.part_empty, (uint32_t)(it - 1) & 1u, &s.abort_flag);
+      if (__any_sync(0xffffffffu, !got)) {
+        set_abort(&s.abort_flag, p.status);
+        break;
+      }
+      tc_fence_after();
+      const uint32_t acc = tmem + (uint32_t)(it & 1) * C::kAccCols + ((uint32_t)(q * 32) << 16);
+#pragma unroll
+      for (int c = 0; c < kTok; c += 16) {
+        if (c >= t.rows_valid) break;
+        uint32_t v[16];
+        tmem_ld_32x32b_x16(acc + c, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s.part[c + i][q * 32 + lane] = __uint_as_float(v[i]);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.acc_empty[it & 1]);
+      if (split == 1) {
+        if (lane == 0) mbar_arrive(&s.part_full);
+      } else if (lane < split) {
+        mbar_arrive_rank_release(&s.part_full, lane);
+      }
+      const bool all = wait_cluster(&s.part_full, (uint32_t)it & 1u, &s.abort_flag);
+      if (__any_sync(0xffffffffu, !all)) {
+        set_abort(&s.abort_flag, p.status);
+        break;
+      }
+      const int col = t.b0 + 4 * lane;
+      if (col < p.J) {                     // J is a multiple of 8
+        for (int r = rank + split * q; r < t.rows_valid; r += 4 * split) {
+          float4 v;
+          if (split == 1) {
+            v = *reinterpret_cast<const float4*>(&s.part[r][4 * lane]);
+          } else {
+            v = make_float4(0.f, 0.f, 0.f, 0.f);
+            const uint32_t at = smem_u32(&s.part[r][4 * lane]);
+            for (int c = 0; c < split; ++c) {
+              const float4 o = ld_cluster_f4(map_rank(at, c));
+              v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+            }
+          }
+          store4(p, v, (t.out_row + r) * (int64_t)p.J + col, col);
+        }
+      }
+      __syncwarp();
+      if (split == 1) {
+        if (lane == 0) mbar_arrive(&s.part_empty);
+      } else if (lane < split) {
+        mbar_arrive_rank(&s.part_empty, lane);
+      }
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  if (split > 1) cluster_sync(); else __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
+}
+
 // One thread per expert: its segment from the offsets, and the scan of the row tiles.
 __global__ void __launch_bounds__(kMaxGroups) mm_table_kernel(const int32_t* offsets, int E, int64_t rows,
                                                               int tile_rows, MmTable t, uint32_t* status) {
@@ -524,7 +776,66 @@ cudaError_t launch_pair(const void* a, const void* b, const MmArgs& m, cudaStrea
                     smem, stream, map_a, map_b, m);
 }
 
+template <int kMode, int kTok>
+cudaError_t launch_narrow(const void* a, const void* b, const MmArgs& m, int split, cudaStream_t stream) {
+  CUtensorMap map_w, map_x;
+  const int err = (kMode == kMmForward ? make_tma_16(&map_w, b, m.R, m.J, m.E, kHalf)
+                                       : make_tma_16(&map_w, b, m.J, m.R, m.E, kBK)) |
+                  make_tma_16(&map_x, a, m.R, m.rows, 1, kTok);
+  if (err != 0) return cudaErrorInvalidValue;
+  const size_t smem = sizeof(NarrowSmem<kTok>) + 1024;
+  static_assert(sizeof(NarrowSmem<kTok>) + 1024 <= 232448, "shared memory exceeds the per-block limit");
+  auto kernel = mm_narrow_kernel<kMode, kTok>;
+  const cudaError_t ce = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (ce != cudaSuccess) return ce;
+  int64_t most = (m.rows + kTok - 1) / kTok;
+  if (m.seg != nullptr) most += m.E < m.rows ? m.E : m.rows;
+  most *= (m.J + kHalf - 1) / kHalf;
+  const int64_t room = num_sms() / split;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((most < room ? most : room) * split));
+  cfg.blockDim = dim3(kNarrowThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = split > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, map_w, map_x, m, split);
+}
+
+template <int kMode>
+cudaError_t launch_rows(const void* a, const void* b, const MmArgs& m, cudaStream_t stream) {
+  const MmPlan plan = mm_plan(m.rows, m.E, m.J, m.R, m.seg != nullptr);
+  switch (plan.tile_rows) {
+    case 16: return launch_narrow<kMode, 16>(a, b, m, plan.split, stream);
+    case 32: return launch_narrow<kMode, 32>(a, b, m, plan.split, stream);
+    case 64: return launch_narrow<kMode, 64>(a, b, m, plan.split, stream);
+    case 128: return launch_narrow<kMode, 128>(a, b, m, plan.split, stream);
+    default: return launch_pair<kMode>(a, b, m, stream);
+  }
+}
+
 }  // namespace
+
+MmPlan mm_plan(int64_t rows, int E, int J, int R, bool ragged) {
+  MmPlan plan{kPairTile, 1};
+  const int64_t mean = (rows + E - 1) / E;     // the split among the experts is known on the device only
+  if (mean > 128) return plan;
+  plan.tile_rows = mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 ? 64 : 128;
+  const int64_t row_tiles = ragged ? (E < rows ? E : rows) : (rows + plan.tile_rows - 1) / plan.tile_rows;
+  const int64_t tiles = row_tiles * ((J + kHalf - 1) / kHalf);
+  const int64_t steps = (R + kBK - 1) / kBK;
+  int64_t split = tiles > 0 ? 148 / tiles : 1;
+  if (split > steps / 4) split = steps / 4;
+  plan.split = (int)(split < 1 ? 1 : split > kMaxSplit ? kMaxSplit : split);
+  return plan;
+}
 
 cudaError_t launch_mm_table(const int32_t* offsets, int E, int64_t rows, int tile_rows, const MmTable& t,
                             uint32_t* status, cudaStream_t stream) {
@@ -534,8 +845,8 @@ cudaError_t launch_mm_table(const int32_t* offsets, int E, int64_t rows, int til
 
 cudaError_t launch_mm(int mode, const void* a, const void* b, const MmArgs& m, cudaStream_t stream) {
   switch (mode) {
-    case kMmForward: return launch_pair<kMmForward>(a, b, m, stream);
-    case kMmDgrad: return launch_pair<kMmDgrad>(a, b, m, stream);
+    case kMmForward: return launch_rows<kMmForward>(a, b, m, stream);
+    case kMmDgrad: return launch_rows<kMmDgrad>(a, b, m, stream);
     default: return launch_pair<kMmWgrad>(a, b, m, stream);
   }
 }

@@ -8,7 +8,6 @@
 
 namespace nvfp4moe {
 
-constexpr int kMmTileRows = 256;       // token rows of a tile (forward, dgrad)
 constexpr int kMaxGroups = 1024;       // experts of one grouped product (one thread each in the table kernel)
 
 // D[i][j] = sum_r A[i][r] B[j][r], per segment (expert) e:
@@ -43,6 +42,14 @@ struct MmArgs {
   void* z_out;           // [rows][J] or nullptr: the sums with the bias, before the activation
   uint32_t* status;
 };
+
+// How forward and dgrad run: token rows of a tile (16 to 128: one CTA a tile, `split` CTAs share its
+// reduction; 256: CTA pairs).  J output columns, R the reduction length.
+struct MmPlan {
+  int tile_rows;
+  int split;
+};
+MmPlan mm_plan(int64_t rows, int E, int J, int R, bool ragged);
 
 // Zeroes the status word and, with offsets, checks them and writes the segment table for row
 // tiles of tile_rows.  Offsets that decrease or leave 0 .. rows raise kStatusBadInput and leave

@@ -48,6 +48,30 @@ __device__ __forceinline__ void store8(const MmArgs& p, float* v, const float* b
       pack16(v[0], v[1], fp16), pack16(v[2], v[3], fp16), pack16(v[4], v[5], fp16), pack16(v[6], v[7], fp16));
 }
 
+// Four consecutive output columns of one row (16-bit output).
+__device__ __forceinline__ void store4(const MmArgs& p, float4 f, int64_t at, int col) {
+  const bool fp16 = p.fp16 != 0;
+  float v[4] = {f.x, f.y, f.z, f.w};
+  if (p.bias != nullptr) {
+    const float4 b = __ldg(reinterpret_cast<const float4*>(p.bias + col));
+    v[0] += b.x; v[1] += b.y; v[2] += b.z; v[3] += b.w;
+  }
+  if (p.z_out != nullptr)
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.z_out) + at) =
+        make_uint2(pack16(v[0], v[1], fp16), pack16(v[2], v[3], fp16));
+  if (p.act != NVFP4MOE_ACT_NONE) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = act_value(v[i], p.act);
+  }
+  if (p.residual != nullptr) {
+    const uint2 r = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.residual) + at);
+    const float2 f0 = unpack16(r.x, fp16), f1 = unpack16(r.y, fp16);
+    v[0] += f0.x; v[1] += f0.y; v[2] += f1.x; v[3] += f1.y;
+  }
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) =
+      make_uint2(pack16(v[0], v[1], fp16), pack16(v[2], v[3], fp16));
+}
+
 // acc: 32 accumulator columns of this lane's row (lane = row); `live` rows from out_row on and the
 // columns below J are stored, 64-byte row pieces at a time.
 __device__ __forceinline__ void store_rows32(EpilogueTile& tile, const uint32_t* acc, const MmArgs& p, int64_t out_row,
