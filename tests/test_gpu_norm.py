@@ -40,7 +40,7 @@ def check(got, want, err, what):
 
 
 SHAPES = [(1, 1), (3, 2), (5, 7), (2, 8), (9, 63), (130, 64), (33, 250), (4, 256), (7, 1000), (65, 1016), (3, 1017),
-          (5, 2048), (4, 2049), (16, 5120), (3, 8192), (2, 8200), (3, 8193), (2, 16384), (3, 16386), (2, 28671),
+          (5, 2048), (4, 2049), (9, 2571), (700, 3001), (16, 5120), (3, 8192), (2, 8200), (3, 8193), (2, 16384), (3, 16386), (2, 28671),
           (2, 28672), (700, 40), (1201, 96)]
 
 
