@@ -430,7 +430,7 @@ ProductWs carve_linear_backward(void* ws, int64_t M, int32_t N) {
 cudaError_t start_product(const ProductWs& p, const int32_t* offsets, int E, int64_t M, int J, int R, cudaStream_t s) {
   g_last_status = p.hdr;
   const int tile_rows = mm_plan(M, E, J, R, offsets != nullptr).tile_rows;
-  const cudaError_t e = launch_mm_table(offsets, E, M, tile_rows, MmTable{p.seg, p.tiles}, &p.hdr->status, s);
+  const cudaError_t e = launch_mm_table(offsets, E, M, tile_rows, MmTable{p.seg, p.tiles}, p.hdr, s);
   if (e == cudaSuccess) ++g_launches;
   return e;
 }
@@ -443,6 +443,7 @@ MmArgs product_args(const ProductWs& p, bool ragged, int E, int64_t M, int32_t d
   m.rows = M;
   m.fp16 = dtype == NVFP4MOE_FP16;
   m.status = &p.hdr->status;
+  m.work_counter = &p.hdr->work[0];
   return m;
 }
 
@@ -467,6 +468,7 @@ cudaError_t product_gradients(const MmArgs& base, const void* dy, const void* x,
     m.J = K;
     m.out = dw;
     m.out_f32 = dw_dtype == NVFP4MOE_FP32;
+    m.work_counter = base.work_counter + 1;
     e = launch_mm(kMmWgrad, dy, x, m, s);
     if (e == cudaSuccess) ++g_launches;
   }

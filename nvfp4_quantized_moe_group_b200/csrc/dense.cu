@@ -10,16 +10,19 @@
 // along memory is K-major in shared memory, one whose i or j does is MN-major (the transposed
 // read is the tensor core's: no operand is ever transposed in memory).
 //
-// A pair of CTAs (one on each SM of a TPC) computes a 256 x 256 tile: each loads its 128 rows of
-// A and its 128 rows of B (32 KB per 64-deep step, 6 stages), tcgen05.mma.cta_group::2 reads
-// both halves of B from both shared memories, and each CTA holds its 128 x 256 FP32 accumulator
-// in tensor memory, double buffered, so the epilogue of one tile overlaps the next one's MMAs.
+// A pair of CTAs (one on each SM of a TPC) computes a tile of up to 256 x 256: each loads its half
+// of A's and of B's rows (32 KB per 64-deep step, 5 stages; 6 measured the same, 4 4 % slower at
+// 4096 x 5120 x 5120), tcgen05.mma.cta_group::2 reads both halves of B from both shared memories,
+// and each CTA holds its 128 x 256 FP32 accumulator in tensor memory, double buffered, so the
+// epilogue of one tile overlaps the next one's MMAs.  In forward and dgrad the 256 features of the
+// weights are the instruction's M side and the token rows its N side: N follows a segment's last rows
+// in steps of 32, so a ragged segment costs tensor time for its own rows only.
 //
 // Per CTA: warp 0 loads (TMA, 128-byte swizzle), both CTAs' bytes counted on the first CTA's
-// barrier; warp 1 of the first CTA issues the MMAs; warps 4-7 run the epilogue through a padded
-// shared-memory tile, so that global accesses are whole 64-byte row pieces.
+// barrier; warp 1 of the first CTA issues the MMAs; warps 4-11 run the epilogue through padded
+// shared-memory tiles, so that global accesses are whole 64-byte row pieces.
 //
-// Ragged ends.  In forward and dgrad, rows behind a segment's end only feed accumulator rows that
+// Ragged ends.  In forward and dgrad, rows behind a segment's end only feed accumulator columns that
 // are not stored.  In wgrad the reduction runs over rows, so the last step of a segment would add
 // rows of the next one (or rows never written, where a NaN passes even a zero factor): warp 2 of
 // each CTA zeroes the lines behind the end in both operands before that step's MMAs.  A row is a
@@ -42,8 +45,9 @@ namespace {
 constexpr int kBK = 64;                  // reduction values per stage (one 128-byte swizzle row)
 constexpr int kPairTile = 256;           // rows and columns of a pair's tile
 constexpr int kHalf = 128;               // each CTA's share of A rows and of B rows
-constexpr int kPairStages = 6;
-constexpr int kPairThreads = 256;
+constexpr int kPairStages = 5;
+constexpr int kPairEpiWarps = 8;
+constexpr int kPairThreads = 128 + 32 * kPairEpiWarps;
 constexpr int kOperandBytes = kHalf * kBK * 2;
 constexpr int kRasterRows = 16;          // row tiles that share a column tile before the next one
 
@@ -98,6 +102,14 @@ __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, con
       return false;
   }
   return true;
+}
+
+// Stores v at this CTA's address `dst` in CTA `rank` and counts the 4 bytes on that CTA's barrier.
+__device__ __forceinline__ void store_rank(int* dst, uint64_t* bar, uint32_t rank, int v) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(
+                   map_rank(smem_u32(dst), rank)),
+               "r"(v), "r"(map_rank(smem_u32(bar), rank))
+               : "memory");
 }
 
 __device__ __forceinline__ void set_abort(int* flag, uint32_t* status) {
@@ -224,10 +236,13 @@ __device__ __forceinline__ Tile tile_at(const MmArgs& p, int w, int tile_i, int 
     t.steps = (int)((seg_rows + kBK - 1) / kBK);
     t.tail = (int)(seg_rows - (int64_t)(t.steps - 1) * kBK);
   } else {
-    const int64_t left = seg_rows - (int64_t)mt * tile_i;
-    t.a0 = seg_row + mt * tile_i;
+    // the segment's rows in equal shares of whole 32 (16 with 16-row tiles): no tile is a small rest
+    const int64_t grain = tile_i < 32 ? tile_i : 32;
+    const int64_t share = ((seg_rows + mt_e - 1) / mt_e + grain - 1) / grain * grain;
+    const int64_t left = seg_rows - mt * share;
+    t.a0 = seg_row + (int)(mt * share);
     t.out_row = t.a0;
-    t.rows_valid = left < tile_i ? (int)left : tile_i;
+    t.rows_valid = left < share ? (int)left : (int)share;
     t.r0 = 0;
     t.steps = (p.R + kBK - 1) / kBK;
     t.tail = kBK;
@@ -235,10 +250,17 @@ __device__ __forceinline__ Tile tile_at(const MmArgs& p, int w, int tile_i, int 
   return t;
 }
 
+// Token rows of a tile as the instruction's N: 32, 64, ... 256.
+__device__ __forceinline__ int pair_columns(int rows) { return (rows + 31) & ~31; }
+
+// Tiles are handed out from a counter of the grid (the first is the pair's own index): tiles differ
+// in cost, so a fixed assignment left pairs idle (64 experts of skewed sizes, 32768 rows: 803 us).
+constexpr int kWorkRing = 4;             // tiles the loads may run ahead of the epilogue
+
 struct __align__(1024) PairSmem {
   uint8_t a[kPairStages][kOperandBytes];
   uint8_t b[kPairStages][kOperandBytes];
-  EpilogueTile epi[4];
+  EpilogueTile epi[kPairEpiWarps];
   uint64_t full[kPairStages];        // (first CTA) both CTAs' loads of the stage have landed
   uint64_t tail_full[kPairStages];   // this CTA's loads of a ragged last step have landed
   uint64_t tail_ready[kPairStages];  // (first CTA) both CTAs have zeroed the rows behind it
@@ -246,16 +268,36 @@ struct __align__(1024) PairSmem {
   uint64_t acc_full[2];
   uint64_t acc_empty[2];         // (first CTA) both CTAs' epilogues have read the accumulator
   uint64_t drain;
+  uint64_t work_full[kWorkRing];     // the slot's tile has arrived
+  uint64_t work_empty[kWorkRing];    // (first CTA) every reader in both CTAs has it
+  int work[kWorkRing];               // tile index, -1: no more
   uint32_t tmem_base;
   int abort_flag;
 };
 
+// The next tile of a reader (a whole warp, or one thread): -1 when there are no more, -2 when the wait
+// ran out.  Frees the slot once every lane has read it.
+template <bool kWarp>
+__device__ __forceinline__ int next_tile(PairSmem& s, int it, int lane) {
+  const int slot = it & (kWorkRing - 1);
+  bool got = wait_cluster(&s.work_full[slot], (uint32_t)(it / kWorkRing) & 1u, &s.abort_flag);
+  if (kWarp) got = __all_sync(0xffffffffu, got);
+  if (!got) return -2;
+  const int w = *reinterpret_cast<volatile int*>(&s.work[slot]);
+  if (kWarp) __syncwarp();
+  if (!kWarp || lane == 0) mbar_arrive_rank(&s.work_empty[slot], 0);
+  return w;
+}
+
 template <int kMode>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+               const __grid_constant__ CUtensorMap map_b64, const __grid_constant__ CUtensorMap map_b32,
                const __grid_constant__ MmArgs p) {
-  constexpr bool kAMn = kMode == kMmWgrad;
-  constexpr bool kBMn = kMode != kMmForward;
+  // forward, dgrad: A = the weights (i: output features), B = the token rows (j)
+  constexpr bool kTokens = kMode != kMmWgrad;
+  constexpr bool kAMn = kMode != kMmForward;
+  constexpr bool kBMn = kMode == kMmWgrad;
   extern __shared__ uint8_t smem_raw[];
   PairSmem& s = *reinterpret_cast<PairSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -272,9 +314,14 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.acc_full[i], 1);
-      mbar_init(&s.acc_empty[i], 8);
+      mbar_init(&s.acc_empty[i], 2 * kPairEpiWarps);
     }
     mbar_init(&s.drain, 1);
+    for (int i = 0; i < kWorkRing; ++i) {
+      mbar_init(&s.work_full[i], 1);
+      // MMA issuer, the second CTA's loads, both CTAs' epilogue warps (and zeroing warps)
+      mbar_init(&s.work_empty[i], 2 + 2 * kPairEpiWarps + (kTokens ? 0 : 2));
+    }
     s.abort_flag = 0;
     fence_barrier_init();
     prefetch_tmap(&map_a);
@@ -297,9 +344,37 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     if (elect_one()) {
       uint32_t stage = 0, phase = 0;
       bool ok = true;
-      for (int w = pair; ok && w < total; w += pairs) {
+      for (int it = 0; ok; ++it) {
+        const int slot = it & (kWorkRing - 1);
+        int w;
+        if (rank == 0) {
+          if (!wait_cluster(&s.work_empty[slot], ((uint32_t)(it / kWorkRing) & 1u) ^ 1u, &s.abort_flag)) {
+            set_abort(&s.abort_flag, p.status);
+            ok = false;
+            break;
+          }
+          w = it == 0 ? pair : pairs + atomicAdd(p.work_counter, 1);
+          if (w >= total) w = -1;
+          store_rank(&s.work[slot], &s.work_full[slot], 1, w);
+          s.work[slot] = w;
+          mbar_arrive(&s.work_full[slot]);
+        } else {
+          mbar_arrive_expect_tx(&s.work_full[slot], 4);
+          w = next_tile<false>(s, it, lane);
+          if (w == -2) {
+            set_abort(&s.abort_flag, p.status);
+            ok = false;
+          }
+        }
+        if (w < 0) break;
         const Tile t = tile_at<kMode>(p, w, kPairTile, kPairTile);
-        const int ai = t.a0 + (int)rank * kHalf, bj = t.b0 + (int)rank * kHalf;
+        // wgrad: 128 rows of each operand; else 128 features, and half of the tile's token rows in
+        // the smallest box that covers them
+        const int half = kTokens ? pair_columns(t.rows_valid) / 2 : kHalf;
+        const int ai = (kTokens ? t.b0 : t.a0) + (int)rank * kHalf;
+        const int bj = (kTokens ? t.a0 : t.b0) + (int)rank * half;
+        const void* mb = half > 64 ? &map_b : half > 32 ? &map_b64 : &map_b32;
+        const uint32_t b_bytes = (half > 64 ? kHalf : half > 32 ? 64 : 32) * kBK * 2;
         for (int k = 0; k < t.steps; ++k) {
           if (!wait_cluster(&s.empty[stage], phase ^ 1u, &s.abort_flag)) {
             set_abort(&s.abort_flag, p.status);
@@ -312,21 +387,21 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             mbar_arrive_expect_tx(&s.tail_full[stage], 2 * kOperandBytes);
             bar = smem_u32(&s.tail_full[stage]);
           } else if (rank == 0) {
-            mbar_arrive_expect_tx(&s.full[stage], 4 * kOperandBytes);
+            mbar_arrive_expect_tx(&s.full[stage], 2 * (kOperandBytes + b_bytes));
           }
           const int r = t.r0 + k * kBK;
+          const int ae = kTokens ? t.e : 0;
           if constexpr (kAMn) {
-            tma_load_pair(s.a[stage], &map_a, bar, ai, r, 0);
-            tma_load_pair(s.a[stage] + kOperandBytes / 2, &map_a, bar, ai + 64, r, 0);
+            tma_load_pair(s.a[stage], &map_a, bar, ai, r, ae);
+            tma_load_pair(s.a[stage] + kOperandBytes / 2, &map_a, bar, ai + 64, r, ae);
           } else {
-            tma_load_pair(s.a[stage], &map_a, bar, r, ai, 0);
+            tma_load_pair(s.a[stage], &map_a, bar, r, ai, ae);
           }
           if constexpr (kBMn) {
-            const int be = kMode == kMmWgrad ? 0 : t.e;
-            tma_load_pair(s.b[stage], &map_b, bar, bj, r, be);
-            tma_load_pair(s.b[stage] + kOperandBytes / 2, &map_b, bar, bj + 64, r, be);
+            tma_load_pair(s.b[stage], &map_b, bar, bj, r, 0);
+            tma_load_pair(s.b[stage] + kOperandBytes / 2, &map_b, bar, bj + 64, r, 0);
           } else {
-            tma_load_pair(s.b[stage], &map_b, bar, r, bj, t.e);
+            tma_load_pair(s.b[stage], mb, bar, r, bj, 0);
           }
           if (++stage == kPairStages) { stage = 0; phase ^= 1u; }
         }
@@ -343,12 +418,18 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     __syncwarp();
     if (rank == 0 && elect_one()) {
       uint32_t stage = 0, phase = 0, tail_par = 0;
-      const uint32_t idesc = idesc_f16(2 * kHalf, kPairTile, p.fp16 != 0, kAMn, kBMn);
       bool ok = true;
-      int it = 0;
-      for (int w = pair; ok && w < total; w += pairs) {
+      int it = 0;                            // tiles with an accumulator
+      for (int n = 0; ok; ++n) {
+        const int w = next_tile<false>(s, n, lane);
+        if (w < 0) {
+          if (w == -2) set_abort(&s.abort_flag, p.status);
+          break;
+        }
         const Tile t = tile_at<kMode>(p, w, kPairTile, kPairTile);
         if (t.steps == 0) continue;
+        const uint32_t idesc =
+            idesc_f16(2 * kHalf, kTokens ? pair_columns(t.rows_valid) : kPairTile, p.fp16 != 0, kAMn, kBMn);
         const uint32_t acc = tmem + (uint32_t)(it & 1) * kPairTile;
         if (!wait_cluster(&s.acc_empty[it & 1], ((uint32_t)(it >> 1) & 1u) ^ 1u, &s.abort_flag)) {
           set_abort(&s.abort_flag, p.status);
@@ -389,7 +470,12 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
   } else if (kMode == kMmWgrad && warp == 2) {
     // ------------------------------------------- rows behind a segment's end ----
     uint32_t stage = 0, tail_par = 0;
-    for (int w = pair; w < total; w += pairs) {
+    for (int n = 0;; ++n) {
+      const int w = next_tile<true>(s, n, lane);
+      if (w < 0) {
+        if (w == -2) set_abort(&s.abort_flag, p.status);
+        break;
+      }
       const Tile t = tile_at<kMode>(p, w, kPairTile, kPairTile);
       if (t.steps == 0) continue;
       const uint32_t at = (stage + (uint32_t)t.steps - 1) % kPairStages;     // the last step's stage
@@ -418,12 +504,17 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     }
   } else if (warp >= 4) {
     // ----------------------------------------------------------- epilogue ----
-    const int q = warp & 3;
-    int it = 0;
-    for (int w = pair; w < total; w += pairs) {
+    const int q = warp & 3;                  // tensor-memory lane quarter this warp may read
+    const int part = (warp - 4) >> 2;        // which of the quarter's two warps
+    EpilogueTile& tile = s.epi[warp - 4];
+    int it = 0;                              // tiles with an accumulator
+    for (int n = 0;; ++n) {
+      const int w = next_tile<true>(s, n, lane);
+      if (w < 0) {
+        if (w == -2) set_abort(&s.abort_flag, p.status);
+        break;
+      }
       const Tile t = tile_at<kMode>(p, w, kPairTile, kPairTile);
-      const int row0 = (int)rank * kHalf + q * 32;          // this warp's rows of the tile
-      const int live = t.rows_valid - row0;                 // of its 32 rows, those to store
       const bool has_acc = t.steps > 0;
       if (has_acc) {
         const bool got = wait_cluster(&s.acc_full[it & 1], (uint32_t)(it >> 1) & 1u, &s.abort_flag);
@@ -434,18 +525,33 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         tc_fence_after();
       }
       const uint32_t acc = tmem + (uint32_t)(it & 1) * kPairTile + ((uint32_t)(q * 32) << 16);
-      const int cols = p.J - t.b0 < kPairTile ? p.J - t.b0 : kPairTile;
-      if (live > 0) {
-        for (int c = 0; c < cols; c += 32) {
-          uint32_t v[32];
-          if (has_acc) {
+      const int lane0 = (int)rank * kHalf + q * 32;        // this warp's first accumulator lane in the tile
+      // the warps of a quarter take its 32-column pieces in turn
+      if constexpr (kTokens) {
+        if (t.b0 + lane0 < p.J) {
+          for (int c = 32 * part; c < t.rows_valid; c += 64) {
+            uint32_t v[32];
             tmem_ld_32x32b_x32(acc + c, v);
             tmem_ld_wait();
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0u;
+            put_columns32(tile, v, lane);
+            store_tile32(tile, p, t.out_row + c, t.rows_valid - c, t.b0 + lane0, lane);
           }
-          store_rows32(s.epi[q], v, p, t.out_row + row0, live, t.b0 + c, lane);
+        }
+      } else {
+        const int live = t.rows_valid - lane0;             // of this warp's 32 rows, those to store
+        if (live > 0) {
+          for (int c = 32 * part; c < kPairTile && t.b0 + c < p.J; c += 64) {
+            uint32_t v[32];
+            if (has_acc) {
+              tmem_ld_32x32b_x32(acc + c, v);
+              tmem_ld_wait();
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = 0u;
+            }
+            put_rows32(tile, v, lane);
+            store_tile32(tile, p, t.out_row + lane0, live, t.b0 + c, lane);
+          }
         }
       }
       if (has_acc) {
@@ -718,7 +824,7 @@ mm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
 
 // One thread per expert: its segment from the offsets, and the scan of the row tiles.
 __global__ void __launch_bounds__(kMaxGroups) mm_table_kernel(const int32_t* offsets, int E, int64_t rows,
-                                                              int tile_rows, MmTable t, uint32_t* status) {
+                                                              int tile_rows, MmTable t, WsHeader* hdr) {
   __shared__ int warp_sum[32];
   pdl_wait();
   pdl_trigger();
@@ -729,7 +835,10 @@ __global__ void __launch_bounds__(kMaxGroups) mm_table_kernel(const int32_t* off
     hi = offsets[e + 1];
   }
   const bool bad = __syncthreads_or(lo < 0 || hi < lo || hi > rows);
-  if (e == 0) *status = bad ? kStatusBadInput : 0u;
+  if (e == 0) {
+    hdr->status = bad ? kStatusBadInput : 0u;
+    hdr->work[0] = hdr->work[1] = 0;
+  }
   if (offsets == nullptr) return;
   if (bad) lo = hi = 0;
   const int n = (int)((hi - lo + tile_rows - 1) / tile_rows);
@@ -753,14 +862,16 @@ __global__ void __launch_bounds__(kMaxGroups) mm_table_kernel(const int32_t* off
 
 template <int kMode>
 cudaError_t launch_pair(const void* a, const void* b, const MmArgs& m, cudaStream_t stream) {
-  CUtensorMap map_a, map_b;
+  CUtensorMap map_a, map_b, map_b64, map_b32;
   int err;
   if (kMode == kMmWgrad) {
     err = make_tma_16(&map_a, a, m.I, m.rows, 1, kBK) | make_tma_16(&map_b, b, m.J, m.rows, 1, kBK);
+    map_b64 = map_b32 = map_b;
   } else {
-    err = make_tma_16(&map_a, a, m.R, m.rows, 1, kHalf);
-    err |= kMode == kMmForward ? make_tma_16(&map_b, b, m.R, m.J, m.E, kHalf)
-                               : make_tma_16(&map_b, b, m.J, m.R, m.E, kBK);
+    err = kMode == kMmForward ? make_tma_16(&map_a, b, m.R, m.J, m.E, kHalf)
+                              : make_tma_16(&map_a, b, m.J, m.R, m.E, kBK);
+    err |= make_tma_16(&map_b, a, m.R, m.rows, 1, kHalf) | make_tma_16(&map_b64, a, m.R, m.rows, 1, 64) |
+           make_tma_16(&map_b32, a, m.R, m.rows, 1, 32);
   }
   if (err != 0) return cudaErrorInvalidValue;
   const size_t smem = sizeof(PairSmem) + 1024;
@@ -773,7 +884,7 @@ cudaError_t launch_pair(const void* a, const void* b, const MmArgs& m, cudaStrea
   most *= ntj;
   const int64_t pairs = num_sms() / 2;
   return launch_pdl(mm_pair_kernel<kMode>, dim3((unsigned)(2 * (most < pairs ? most : pairs))), dim3(kPairThreads),
-                    smem, stream, map_a, map_b, m);
+                    smem, stream, map_a, map_b, map_b64, map_b32, m);
 }
 
 template <int kMode, int kTok>
@@ -838,9 +949,9 @@ MmPlan mm_plan(int64_t rows, int E, int J, int R, bool ragged) {
 }
 
 cudaError_t launch_mm_table(const int32_t* offsets, int E, int64_t rows, int tile_rows, const MmTable& t,
-                            uint32_t* status, cudaStream_t stream) {
+                            WsHeader* hdr, cudaStream_t stream) {
   const int threads = offsets == nullptr ? 32 : (E + 31) / 32 * 32;
-  return launch_pdl(mm_table_kernel, dim3(1), dim3(threads), 0, stream, offsets, E, rows, tile_rows, t, status);
+  return launch_pdl(mm_table_kernel, dim3(1), dim3(threads), 0, stream, offsets, E, rows, tile_rows, t, hdr);
 }
 
 cudaError_t launch_mm(int mode, const void* a, const void* b, const MmArgs& m, cudaStream_t stream) {

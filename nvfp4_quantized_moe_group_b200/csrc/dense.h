@@ -8,6 +8,8 @@
 
 namespace nvfp4moe {
 
+struct WsHeader;
+
 constexpr int kMaxGroups = 1024;       // experts of one grouped product (one thread each in the table kernel)
 
 // D[i][j] = sum_r A[i][r] B[j][r], per segment (expert) e:
@@ -41,6 +43,7 @@ struct MmArgs {
   const void* residual;  // [rows][J] or nullptr, the operands' type
   void* z_out;           // [rows][J] or nullptr: the sums with the bias, before the activation
   uint32_t* status;
+  int* work_counter;     // zero at launch: tiles handed out beyond the first of each CTA pair
 };
 
 // How forward and dgrad run: token rows of a tile (16 to 128: one CTA a tile, `split` CTAs share its
@@ -51,11 +54,11 @@ struct MmPlan {
 };
 MmPlan mm_plan(int64_t rows, int E, int J, int R, bool ragged);
 
-// Zeroes the status word and, with offsets, checks them and writes the segment table for row
+// Zeroes the status word and the work counters and, with offsets, checks them and writes the segment table for row
 // tiles of tile_rows.  Offsets that decrease or leave 0 .. rows raise kStatusBadInput and leave
 // every segment empty, so no later kernel of the call reads or writes through them.
 cudaError_t launch_mm_table(const int32_t* offsets, int E, int64_t rows, int tile_rows, const MmTable& t,
-                            uint32_t* status, cudaStream_t stream);
+                            WsHeader* hdr, cudaStream_t stream);
 // The product.  a, b: the operands' base addresses.
 cudaError_t launch_mm(int mode, const void* a, const void* b, const MmArgs& m, cudaStream_t stream);
 

@@ -72,16 +72,27 @@ __device__ __forceinline__ void store4(const MmArgs& p, float4 f, int64_t at, in
       make_uint2(pack16(v[0], v[1], fp16), pack16(v[2], v[3], fp16));
 }
 
-// acc: 32 accumulator columns of this lane's row (lane = row); `live` rows from out_row on and the
-// columns below J are stored, 64-byte row pieces at a time.
-__device__ __forceinline__ void store_rows32(EpilogueTile& tile, const uint32_t* acc, const MmArgs& p, int64_t out_row,
-                                             int live, int col0, int lane) {
+// 32 accumulator columns of this lane into the tile: the lane is the tile's row ...
+__device__ __forceinline__ void put_rows32(EpilogueTile& tile, const uint32_t* acc, int lane) {
   __syncwarp();   // the previous piece has been read
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     *reinterpret_cast<uint4*>(&tile.v[lane][4 * i]) =
         make_uint4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
   __syncwarp();
+}
+// ... or its column.
+__device__ __forceinline__ void put_columns32(EpilogueTile& tile, const uint32_t* acc, int lane) {
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 32; ++i) tile.v[i][lane] = __uint_as_float(acc[i]);
+  __syncwarp();
+}
+
+// Stores `live` rows of the tile from out_row on, and of its columns (from col0 on) those below J,
+// in 64-byte row pieces.
+__device__ __forceinline__ void store_tile32(const EpilogueTile& tile, const MmArgs& p, int64_t out_row, int live,
+                                             int col0, int lane) {
   const int c8 = (lane & 3) * 8, col = col0 + c8;
   if (col >= p.J) return;          // J is a multiple of 8
   float bias8[8];
