@@ -19,8 +19,11 @@
 // in steps of 32, so a ragged segment costs tensor time for its own rows only.
 //
 // Per CTA: warp 0 loads (TMA, 128-byte swizzle), both CTAs' bytes counted on the first CTA's
-// barrier; warp 1 of the first CTA issues the MMAs; warps 4-11 run the epilogue through padded
-// shared-memory tiles, so that global accesses are whole 64-byte row pieces.
+// barrier; warp 1 of the first CTA issues the MMAs; warps 4-11 run the epilogue: forward and dgrad
+// through padded shared-memory tiles, so that global accesses are whole 64-byte row pieces; wgrad,
+// whose rows are never ragged, by TMA stores of 128-byte x 32-row pieces (an expert's few rows make
+// few steps a tile, so wgrad is bound by its output: 64 experts of 128 rows, 5120 x 2560, 931 us
+// with the padded tiles and plain stores).
 //
 // Ragged ends.  In forward and dgrad, rows behind a segment's end only feed accumulator columns that
 // are not stored.  In wgrad the reduction runs over rows, so the last step of a segment would add
@@ -253,6 +256,32 @@ __device__ __forceinline__ Tile tile_at(const MmArgs& p, int w, int tile_i, int 
 // Token rows of a tile as the instruction's N: 32, 64, ... 256.
 __device__ __forceinline__ int pair_columns(int rows) { return (rows + 31) & ~31; }
 
+constexpr int kPieceBytes = 32 * 128;    // 32 rows of 128 bytes, 128-byte swizzle
+
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// Until this thread's bulk stores have read shared memory / have been written.
+__device__ __forceinline__ void bulk_wait_read0() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all0() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// Stores 128 bytes of each of 32 rows (this lane's: w) at column c0, row c1 of matrix c2.
+__device__ __forceinline__ void store_piece(const void* tmap, uint8_t* piece, const uint32_t* w, int c0, int c1,
+                                            int c2, int lane) {
+  if (lane == 0) bulk_wait_read0();          // the piece before has been read
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    *reinterpret_cast<uint4*>(piece + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+        make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+  if (lane == 0) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(tmap),
+                 "r"(smem_u32(piece)), "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+    bulk_commit();
+  }
+}
+
 // Tiles are handed out from a counter of the grid (the first is the pair's own index): tiles differ
 // in cost, so a fixed assignment left pairs idle (64 experts of skewed sizes, 32768 rows: 803 us).
 constexpr int kWorkRing = 4;             // tiles the loads may run ahead of the epilogue
@@ -260,7 +289,7 @@ constexpr int kWorkRing = 4;             // tiles the loads may run ahead of the
 struct __align__(1024) PairSmem {
   uint8_t a[kPairStages][kOperandBytes];
   uint8_t b[kPairStages][kOperandBytes];
-  EpilogueTile epi[kPairEpiWarps];
+  uint8_t epi[kPairEpiWarps * sizeof(EpilogueTile)];   // 1024-byte aligned: wgrad's pieces of 4 KB a warp
   uint64_t full[kPairStages];        // (first CTA) both CTAs' loads of the stage have landed
   uint64_t tail_full[kPairStages];   // this CTA's loads of a ragged last step have landed
   uint64_t tail_ready[kPairStages];  // (first CTA) both CTAs have zeroed the rows behind it
@@ -293,7 +322,7 @@ template <int kMode>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                const __grid_constant__ CUtensorMap map_b64, const __grid_constant__ CUtensorMap map_b32,
-               const __grid_constant__ MmArgs p) {
+               const __grid_constant__ CUtensorMap map_out, const __grid_constant__ MmArgs p) {
   // forward, dgrad: A = the weights (i: output features), B = the token rows (j)
   constexpr bool kTokens = kMode != kMmWgrad;
   constexpr bool kAMn = kMode != kMmForward;
@@ -344,6 +373,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     if (elect_one()) {
       uint32_t stage = 0, phase = 0;
       bool ok = true;
+      int next = pair;
       for (int it = 0; ok; ++it) {
         const int slot = it & (kWorkRing - 1);
         int w;
@@ -353,8 +383,9 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             ok = false;
             break;
           }
-          w = it == 0 ? pair : pairs + atomicAdd(p.work_counter, 1);
-          if (w >= total) w = -1;
+          w = next < total ? next : -1;
+          // the one after it, under way while this one's loads are issued
+          if (w >= 0) next = pairs + atomicAdd(p.work_counter, 1);
           store_rank(&s.work[slot], &s.work_full[slot], 1, w);
           s.work[slot] = w;
           mbar_arrive(&s.work_full[slot]);
@@ -506,7 +537,8 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     // ----------------------------------------------------------- epilogue ----
     const int q = warp & 3;                  // tensor-memory lane quarter this warp may read
     const int part = (warp - 4) >> 2;        // which of the quarter's two warps
-    EpilogueTile& tile = s.epi[warp - 4];
+    EpilogueTile& tile = reinterpret_cast<EpilogueTile*>(s.epi)[warp - 4];
+    uint8_t* piece = s.epi + (warp - 4) * kPieceBytes;
     int it = 0;                              // tiles with an accumulator
     for (int n = 0;; ++n) {
       const int w = next_tile<true>(s, n, lane);
@@ -538,19 +570,27 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
           }
         }
       } else {
-        const int live = t.rows_valid - lane0;             // of this warp's 32 rows, those to store
-        if (live > 0) {
-          for (int c = 32 * part; c < kPairTile && t.b0 + c < p.J; c += 64) {
-            uint32_t v[32];
+        if (t.rows_valid > lane0) {            // rows and columns behind the output's are clipped by the map
+          for (int c = 64 * part; c < kPairTile && t.b0 + c < p.J; c += 128) {
+            uint32_t v[64];
             if (has_acc) {
               tmem_ld_32x32b_x32(acc + c, v);
+              tmem_ld_32x32b_x32(acc + c + 32, v + 32);
               tmem_ld_wait();
             } else {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = 0u;
+              for (int i = 0; i < 64; ++i) v[i] = 0u;
             }
-            put_rows32(tile, v, lane);
-            store_tile32(tile, p, t.out_row + lane0, live, t.b0 + c, lane);
+            if (p.out_f32) {
+              store_piece(&map_out, piece, v, t.b0 + c, t.a0 + lane0, t.e, lane);
+              if (t.b0 + c + 32 < p.J) store_piece(&map_out, piece, v + 32, t.b0 + c + 32, t.a0 + lane0, t.e, lane);
+            } else {
+              uint32_t h[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                h[i] = pack16(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), p.fp16 != 0);
+              store_piece(&map_out, piece, h, t.b0 + c, t.a0 + lane0, t.e, lane);
+            }
           }
         }
       }
@@ -561,6 +601,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         ++it;
       }
     }
+    if (kMode == kMmWgrad && lane == 0) bulk_wait_all0();
   }
 
   __syncwarp();
@@ -862,16 +903,18 @@ __global__ void __launch_bounds__(kMaxGroups) mm_table_kernel(const int32_t* off
 
 template <int kMode>
 cudaError_t launch_pair(const void* a, const void* b, const MmArgs& m, cudaStream_t stream) {
-  CUtensorMap map_a, map_b, map_b64, map_b32;
+  CUtensorMap map_a, map_b, map_b64, map_b32, map_out;
   int err;
   if (kMode == kMmWgrad) {
-    err = make_tma_16(&map_a, a, m.I, m.rows, 1, kBK) | make_tma_16(&map_b, b, m.J, m.rows, 1, kBK);
+    err = make_tma_16(&map_a, a, m.I, m.rows, 1, kBK) | make_tma_16(&map_b, b, m.J, m.rows, 1, kBK) |
+          make_tma_3d(&map_out, m.out, m.out_f32 ? 4 : 2, m.J, m.I, m.E, 32);
     map_b64 = map_b32 = map_b;
   } else {
     err = kMode == kMmForward ? make_tma_16(&map_a, b, m.R, m.J, m.E, kHalf)
                               : make_tma_16(&map_a, b, m.J, m.R, m.E, kBK);
     err |= make_tma_16(&map_b, a, m.R, m.rows, 1, kHalf) | make_tma_16(&map_b64, a, m.R, m.rows, 1, 64) |
            make_tma_16(&map_b32, a, m.R, m.rows, 1, 32);
+    map_out = map_b;       // not used: ragged rows cannot be clipped by a map
   }
   if (err != 0) return cudaErrorInvalidValue;
   const size_t smem = sizeof(PairSmem) + 1024;
@@ -884,7 +927,7 @@ cudaError_t launch_pair(const void* a, const void* b, const MmArgs& m, cudaStrea
   most *= ntj;
   const int64_t pairs = num_sms() / 2;
   return launch_pdl(mm_pair_kernel<kMode>, dim3((unsigned)(2 * (most < pairs ? most : pairs))), dim3(kPairThreads),
-                    smem, stream, map_a, map_b, map_b64, map_b32, m);
+                    smem, stream, map_a, map_b, map_b64, map_b32, map_out, m);
 }
 
 template <int kMode, int kTok>

@@ -68,8 +68,13 @@ int act_grad_partials(int64_t M, int64_t N);
 cudaError_t launch_act_grad(const void* dy, const void* z, int64_t M, int N, int act, bool fp16, void* dz, float* db,
                             float* partials, int* launches, cudaStream_t stream);
 
-// gemm.cu: tensor map of 16-bit elements [batch][rows][inner], a 64 x box_rows x 1 box, 128B swizzle.
-int make_tma_16(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint64_t batch,
-                uint32_t box_rows);
+// gemm.cu: tensor map of 2- or 4-byte elements [batch][rows][inner], a box of 128 bytes x box_rows x 1, 128B
+// swizzle.
+int make_tma_3d(CUtensorMap* map, const void* base, uint32_t elem_bytes, uint64_t inner, uint64_t rows,
+                uint64_t batch, uint32_t box_rows);
+inline int make_tma_16(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint64_t batch,
+                       uint32_t box_rows) {
+  return make_tma_3d(map, base, 2, inner, rows, batch, box_rows);
+}
 
 }  // namespace nvfp4moe

@@ -8,20 +8,14 @@
 
 namespace nvfp4moe {
 
-// One warp's 32 x 32 FP32 transpose tile; rows 144 bytes apart, so 16-byte accesses of 8 lanes in
-// consecutive rows, and of 8 lanes in two rows, fall in different banks.
+// One warp's 32 x 32 FP32 transpose tile; rows 144 bytes apart, so 16-byte reads of 8 lanes in two
+// rows fall in different banks.
 struct EpilogueTile {
   float v[32][36];
 };
 
-// Eight consecutive output columns of one row: at = row * J + col.
+// Eight consecutive output columns of one row (16-bit output): at = row * J + col.
 __device__ __forceinline__ void store8(const MmArgs& p, float* v, const float* bias8, int64_t at) {
-  if (p.out_f32) {
-    float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
-    o[0] = make_float4(v[0], v[1], v[2], v[3]);
-    o[1] = make_float4(v[4], v[5], v[6], v[7]);
-    return;
-  }
   const bool fp16 = p.fp16 != 0;
   if (p.bias != nullptr) {
 #pragma unroll
@@ -72,18 +66,9 @@ __device__ __forceinline__ void store4(const MmArgs& p, float4 f, int64_t at, in
       make_uint2(pack16(v[0], v[1], fp16), pack16(v[2], v[3], fp16));
 }
 
-// 32 accumulator columns of this lane into the tile: the lane is the tile's row ...
-__device__ __forceinline__ void put_rows32(EpilogueTile& tile, const uint32_t* acc, int lane) {
-  __syncwarp();   // the previous piece has been read
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    *reinterpret_cast<uint4*>(&tile.v[lane][4 * i]) =
-        make_uint4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
-  __syncwarp();
-}
-// ... or its column.
+// 32 accumulator columns of this lane into the tile's column `lane`.
 __device__ __forceinline__ void put_columns32(EpilogueTile& tile, const uint32_t* acc, int lane) {
-  __syncwarp();
+  __syncwarp();   // the previous piece has been read
 #pragma unroll
   for (int i = 0; i < 32; ++i) tile.v[i][lane] = __uint_as_float(acc[i]);
   __syncwarp();
