@@ -400,6 +400,7 @@ struct ProductWs {
   WsHeader* hdr;
   int32_t* seg;
   int32_t* tiles;
+  CUtensorMap* maps;       // grouped calls only
   uint16_t* dz;            // linear_backward only
   float* partials;
   size_t bytes;
@@ -411,6 +412,7 @@ ProductWs carve_product(void* ws, int32_t E) {
   p.hdr = c.take<WsHeader>(1);
   p.seg = c.take<int32_t>(2 * (size_t)E);
   p.tiles = c.take<int32_t>((size_t)E + 1);
+  p.maps = c.take<CUtensorMap>(2 * (size_t)E);
   p.bytes = c.off;
   return p;
 }
@@ -427,10 +429,12 @@ ProductWs carve_linear_backward(void* ws, int64_t M, int32_t N) {
 
 // Resets the status word and builds the segment table of a ragged call (offsets != nullptr).
 // J, R: the columns and reduction length of the call's row product (forward or dgrad).
-cudaError_t start_product(const ProductWs& p, const int32_t* offsets, int E, int64_t M, int J, int R, cudaStream_t s) {
+// wgrad: its operands, when the call runs a ragged one.
+cudaError_t start_product(const ProductWs& p, const int32_t* offsets, int E, int64_t M, int J, int R,
+                          const MmWgradOperands* wgrad, cudaStream_t s) {
   g_last_status = p.hdr;
   const int tile_rows = mm_plan(M, E, J, R, offsets != nullptr).tile_rows;
-  const cudaError_t e = launch_mm_table(offsets, E, M, tile_rows, MmTable{p.seg, p.tiles}, p.hdr, s);
+  const cudaError_t e = launch_mm_table(offsets, E, M, tile_rows, MmTable{p.seg, p.tiles, p.maps}, p.hdr, wgrad, s);
   if (e == cudaSuccess) ++g_launches;
   return e;
 }
@@ -439,6 +443,7 @@ MmArgs product_args(const ProductWs& p, bool ragged, int E, int64_t M, int32_t d
   MmArgs m{};
   m.seg = ragged ? p.seg : nullptr;
   m.tiles = ragged ? p.tiles : nullptr;
+  m.seg_maps = ragged ? p.maps : nullptr;
   m.E = E;
   m.rows = M;
   m.fp16 = dtype == NVFP4MOE_FP16;
@@ -1690,7 +1695,7 @@ int nvfp4moe_grouped_mm(int32_t dtype, const void* x, int64_t M, int32_t K, cons
   const int st = check_device();
   if (st != NVFP4MOE_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (start_product(p, offsets, E, M, N, K, s) != cudaSuccess) return cuda_failed();
+  if (start_product(p, offsets, E, M, N, K, nullptr, s) != cudaSuccess) return cuda_failed();
   if (M == 0) return NVFP4MOE_OK;
   MmArgs m = product_args(p, true, E, M, dtype);
   m.J = N;
@@ -1718,7 +1723,9 @@ int nvfp4moe_grouped_mm_backward(int32_t dtype, const void* dy, const void* x, c
   const int st = check_device();
   if (st != NVFP4MOE_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (start_product(p, offsets, E, M, K, N, s) != cudaSuccess) return cuda_failed();
+  const MmWgradOperands wgrad{dy, x, N, K};
+  if (start_product(p, offsets, E, M, K, N, dw != nullptr && M > 0 ? &wgrad : nullptr, s) != cudaSuccess)
+    return cuda_failed();
   if (product_gradients(product_args(p, true, E, M, dtype), dy, x, w, K, N, dx, dw, dw_dtype, s) != cudaSuccess)
     return cuda_failed();
   return NVFP4MOE_OK;
@@ -1742,7 +1749,7 @@ int nvfp4moe_linear(int32_t dtype, const void* x, int64_t M, int32_t K, const vo
   const int st = check_device();
   if (st != NVFP4MOE_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (start_product(p, nullptr, 1, M, N, K, s) != cudaSuccess) return cuda_failed();
+  if (start_product(p, nullptr, 1, M, N, K, nullptr, s) != cudaSuccess) return cuda_failed();
   if (M == 0) return NVFP4MOE_OK;
   MmArgs m = product_args(p, false, 1, M, dtype);
   m.J = N;
@@ -1781,7 +1788,7 @@ int nvfp4moe_linear_backward(int32_t dtype, const void* dy, const void* x, const
   const int st = check_device();
   if (st != NVFP4MOE_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (start_product(p, nullptr, 1, M, N, K, s) != cudaSuccess) return cuda_failed();
+  if (start_product(p, nullptr, 1, M, N, K, nullptr, s) != cudaSuccess) return cuda_failed();
   if (M == 0) {
     if (db != nullptr && cudaMemsetAsync(db, 0, (size_t)N * sizeof(float), s) != cudaSuccess) return cuda_failed();
   } else if (act != NVFP4MOE_ACT_NONE || db != nullptr) {

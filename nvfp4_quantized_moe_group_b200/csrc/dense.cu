@@ -27,12 +27,10 @@
 //
 // Ragged ends.  In forward and dgrad, rows behind a segment's end only feed accumulator columns that
 // are not stored.  In wgrad the reduction runs over rows, so the last step of a segment would add
-// rows of the next one (or rows never written, where a NaN passes even a zero factor): warp 2 of
-// each CTA zeroes the lines behind the end in both operands before that step's MMAs.  A row is a
-// whole 128-byte line of the MN-major tile, so the range is contiguous whatever the swizzle.  Only
-// such a step takes the extra hop (its own barriers); passing every stage through a
-// release.cluster arrival cost a fence's latency per stage (4096 x 5120 x 5120: 388 us, 150 us
-// without).
+// rows of the next one (or rows never written, where a NaN passes even a zero factor): each
+// segment has tensor maps of its own, built on the device from the offsets, whose row bound makes
+// the loads fill zeros behind its end.  (Zeroing those lines in shared memory before the MMAs
+// cost every tile a cross-CTA fence: 64 skewed experts, 32768 rows, 1011 us.)
 //
 // Every wait is bounded; one that runs out raises the timeout bit of the status word and the
 // pair winds down.
@@ -131,6 +129,11 @@ __device__ __forceinline__ void tma_load_pair(void* dst, const void* tmap, uint3
       : "memory");
 }
 
+// Makes a tensor map written by an earlier kernel usable by this thread's copies.
+__device__ __forceinline__ void acquire_tmap(const void* tmap) {
+  asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(tmap) : "memory");
+}
+
 // ------------------------------------------------------------ tcgen05, CTA pairs ----
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(ncols)
@@ -181,9 +184,7 @@ struct Tile {
   int a0, b0;        // kMmWgrad: first i, first j; else first token row, first j
   int64_t out_row;   // row of D (in the whole output) that a0 is
   int rows_valid;    // rows of the tile to store
-  int r0;            // kMmWgrad: first token row of the reduction
   int steps;         // 64-deep reduction steps
-  int tail;          // valid values of the last step (kMmWgrad)
 };
 
 template <int kMode>
@@ -235,9 +236,7 @@ __device__ __forceinline__ Tile tile_at(const MmArgs& p, int w, int tile_i, int 
     t.a0 = mt * tile_i;
     t.out_row = (int64_t)t.e * p.I + t.a0;
     t.rows_valid = p.I - t.a0 < tile_i ? p.I - t.a0 : tile_i;
-    t.r0 = seg_row;
     t.steps = (int)((seg_rows + kBK - 1) / kBK);
-    t.tail = (int)(seg_rows - (int64_t)(t.steps - 1) * kBK);
   } else {
     // the segment's rows in equal shares of whole 32 (16 with 16-row tiles): no tile is a small rest
     const int64_t grain = tile_i < 32 ? tile_i : 32;
@@ -246,9 +245,7 @@ __device__ __forceinline__ Tile tile_at(const MmArgs& p, int w, int tile_i, int 
     t.a0 = seg_row + (int)(mt * share);
     t.out_row = t.a0;
     t.rows_valid = left < share ? (int)left : (int)share;
-    t.r0 = 0;
     t.steps = (p.R + kBK - 1) / kBK;
-    t.tail = kBK;
   }
   return t;
 }
@@ -291,8 +288,6 @@ struct __align__(1024) PairSmem {
   uint8_t b[kPairStages][kOperandBytes];
   uint8_t epi[kPairEpiWarps * sizeof(EpilogueTile)];   // 1024-byte aligned: wgrad's pieces of 4 KB a warp
   uint64_t full[kPairStages];        // (first CTA) both CTAs' loads of the stage have landed
-  uint64_t tail_full[kPairStages];   // this CTA's loads of a ragged last step have landed
-  uint64_t tail_ready[kPairStages];  // (first CTA) both CTAs have zeroed the rows behind it
   uint64_t empty[kPairStages];   // the MMAs have read the stage
   uint64_t acc_full[2];
   uint64_t acc_empty[2];         // (first CTA) both CTAs' epilogues have read the accumulator
@@ -337,8 +332,6 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
   if (threadIdx.x == 0) {
     for (int i = 0; i < kPairStages; ++i) {
       mbar_init(&s.full[i], 1);
-      mbar_init(&s.tail_full[i], 1);
-      mbar_init(&s.tail_ready[i], 2);
       mbar_init(&s.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -348,8 +341,8 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     mbar_init(&s.drain, 1);
     for (int i = 0; i < kWorkRing; ++i) {
       mbar_init(&s.work_full[i], 1);
-      // MMA issuer, the second CTA's loads, both CTAs' epilogue warps (and zeroing warps)
-      mbar_init(&s.work_empty[i], 2 + 2 * kPairEpiWarps + (kTokens ? 0 : 2));
+      // MMA issuer, the second CTA's loads, both CTAs' epilogue warps
+      mbar_init(&s.work_empty[i], 2 + 2 * kPairEpiWarps);
     }
     s.abort_flag = 0;
     fence_barrier_init();
@@ -373,7 +366,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     if (elect_one()) {
       uint32_t stage = 0, phase = 0;
       bool ok = true;
-      int next = pair;
+      int next = pair, map_e = -1;
       for (int it = 0; ok; ++it) {
         const int slot = it & (kWorkRing - 1);
         int w;
@@ -404,7 +397,17 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         const int half = kTokens ? pair_columns(t.rows_valid) / 2 : kHalf;
         const int ai = (kTokens ? t.b0 : t.a0) + (int)rank * kHalf;
         const int bj = (kTokens ? t.a0 : t.b0) + (int)rank * half;
+        const void* ma = &map_a;
         const void* mb = half > 64 ? &map_b : half > 32 ? &map_b64 : &map_b32;
+        if (!kTokens && p.seg_maps != nullptr && t.steps > 0) {
+          ma = p.seg_maps + 2 * t.e;
+          mb = p.seg_maps + 2 * t.e + 1;
+          if (t.e != map_e) {
+            acquire_tmap(ma);
+            acquire_tmap(mb);
+            map_e = t.e;
+          }
+        }
         const uint32_t b_bytes = (half > 64 ? kHalf : half > 32 ? 64 : 32) * kBK * 2;
         for (int k = 0; k < t.steps; ++k) {
           if (!wait_cluster(&s.empty[stage], phase ^ 1u, &s.abort_flag)) {
@@ -412,25 +415,19 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             ok = false;
             break;
           }
-          uint32_t bar = map_rank(smem_u32(&s.full[stage]), 0);
-          if (kMode == kMmWgrad && k == t.steps - 1 && t.tail < kBK) {
-            if (rank == 0) mbar_arrive(&s.full[stage]);
-            mbar_arrive_expect_tx(&s.tail_full[stage], 2 * kOperandBytes);
-            bar = smem_u32(&s.tail_full[stage]);
-          } else if (rank == 0) {
-            mbar_arrive_expect_tx(&s.full[stage], 2 * (kOperandBytes + b_bytes));
-          }
-          const int r = t.r0 + k * kBK;
+          const uint32_t bar = map_rank(smem_u32(&s.full[stage]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&s.full[stage], 2 * (kOperandBytes + b_bytes));
+          const int r = k * kBK;
           const int ae = kTokens ? t.e : 0;
           if constexpr (kAMn) {
-            tma_load_pair(s.a[stage], &map_a, bar, ai, r, ae);
-            tma_load_pair(s.a[stage] + kOperandBytes / 2, &map_a, bar, ai + 64, r, ae);
+            tma_load_pair(s.a[stage], ma, bar, ai, r, ae);
+            tma_load_pair(s.a[stage] + kOperandBytes / 2, ma, bar, ai + 64, r, ae);
           } else {
-            tma_load_pair(s.a[stage], &map_a, bar, r, ai, ae);
+            tma_load_pair(s.a[stage], ma, bar, r, ai, ae);
           }
           if constexpr (kBMn) {
-            tma_load_pair(s.b[stage], &map_b, bar, bj, r, 0);
-            tma_load_pair(s.b[stage] + kOperandBytes / 2, &map_b, bar, bj + 64, r, 0);
+            tma_load_pair(s.b[stage], mb, bar, bj, r, 0);
+            tma_load_pair(s.b[stage] + kOperandBytes / 2, mb, bar, bj + 64, r, 0);
           } else {
             tma_load_pair(s.b[stage], mb, bar, r, bj, 0);
           }
@@ -448,7 +445,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     // --------------------------------------------------------------- MMAs ----
     __syncwarp();
     if (rank == 0 && elect_one()) {
-      uint32_t stage = 0, phase = 0, tail_par = 0;
+      uint32_t stage = 0, phase = 0;
       bool ok = true;
       int it = 0;                            // tiles with an accumulator
       for (int n = 0; ok; ++n) {
@@ -468,12 +465,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         }
         tc_fence_after();
         for (int k = 0; k < t.steps; ++k) {
-          bool landed = wait_cluster(&s.full[stage], phase, &s.abort_flag);
-          if (kMode == kMmWgrad && k == t.steps - 1 && t.tail < kBK) {
-            landed = landed && wait_cluster(&s.tail_ready[stage], (tail_par >> stage) & 1u, &s.abort_flag);
-            tail_par ^= 1u << stage;
-          }
-          if (!landed) {
+          if (!wait_cluster(&s.full[stage], phase, &s.abort_flag)) {
             set_abort(&s.abort_flag, p.status);
             ok = false;
             break;
@@ -497,41 +489,6 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
       // every tensor-core operation of the pair is done before the memories are given back
       tc_commit_pair(&s.drain);
       if (!mbar_wait(&s.drain, 0)) set_abort(&s.abort_flag, p.status);
-    }
-  } else if (kMode == kMmWgrad && warp == 2) {
-    // ------------------------------------------- rows behind a segment's end ----
-    uint32_t stage = 0, tail_par = 0;
-    for (int n = 0;; ++n) {
-      const int w = next_tile<true>(s, n, lane);
-      if (w < 0) {
-        if (w == -2) set_abort(&s.abort_flag, p.status);
-        break;
-      }
-      const Tile t = tile_at<kMode>(p, w, kPairTile, kPairTile);
-      if (t.steps == 0) continue;
-      const uint32_t at = (stage + (uint32_t)t.steps - 1) % kPairStages;     // the last step's stage
-      stage = (stage + (uint32_t)t.steps) % kPairStages;
-      if (t.tail == kBK) continue;
-      const bool got = wait_cluster(&s.tail_full[at], (tail_par >> at) & 1u, &s.abort_flag);
-      tail_par ^= 1u << at;
-      if (__any_sync(0xffffffffu, !got)) {
-        set_abort(&s.abort_flag, p.status);
-        break;
-      }
-      // lines t.tail .. 63 of the four 64-line blocks
-      const int lines16 = (kBK - t.tail) * 8;
-      const uint4 zero = make_uint4(0, 0, 0, 0);
-      for (int i = lane; i < lines16; i += 32) {
-        uint8_t* dst = s.a[at] + t.tail * 128 + i * 16;
-        *reinterpret_cast<uint4*>(dst) = zero;
-        *reinterpret_cast<uint4*>(dst + kOperandBytes / 2) = zero;
-        dst = s.b[at] + t.tail * 128 + i * 16;
-        *reinterpret_cast<uint4*>(dst) = zero;
-        *reinterpret_cast<uint4*>(dst + kOperandBytes / 2) = zero;
-      }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive_rank_release(&s.tail_ready[at], 0);
     }
   } else if (warp >= 4) {
     // ----------------------------------------------------------- epilogue ----
@@ -863,10 +820,13 @@ mm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
   if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
 }
 
-// One thread per expert: its segment from the offsets, and the scan of the row tiles.
+// One thread per expert: its segment from the offsets, and the scan of the row tiles; then, for wgrad,
+// one warp per tensor map: the map of the whole operand with the segment's first row and row count.
 __global__ void __launch_bounds__(kMaxGroups) mm_table_kernel(const int32_t* offsets, int E, int64_t rows,
-                                                              int tile_rows, MmTable t, WsHeader* hdr) {
+                                                              int tile_rows, MmTable t, WsHeader* hdr,
+                                                              const __grid_constant__ MmSegMaps maps) {
   __shared__ int warp_sum[32];
+  __shared__ __align__(128) uint32_t s_map[32][32];
   pdl_wait();
   pdl_trigger();
   const int e = threadIdx.x, lane = e & 31, warp = e >> 5;
@@ -899,6 +859,31 @@ __global__ void __launch_bounds__(kMaxGroups) mm_table_kernel(const int32_t* off
     t.tiles[e + 1] = before + sum;
   }
   if (e == 0) t.tiles[0] = 0;
+  if (maps.out == nullptr) return;
+  __syncthreads();                        // the segments are written (read back below)
+  for (int m = warp; m < 2 * E; m += blockDim.x >> 5) {
+    const int which = m & 1;
+    const int first = t.seg[2 * (m >> 1)], count = t.seg[2 * (m >> 1) + 1];
+    if (count == 0) continue;             // never loaded from
+    __syncwarp();
+    s_map[warp][lane] = reinterpret_cast<const uint32_t*>(which == 0 ? &maps.a : &maps.b)[lane];
+    __syncwarp();
+    const uint32_t at = smem_u32(s_map[warp]);
+    if (lane == 0) {
+      const uint64_t base = reinterpret_cast<uint64_t>(which == 0 ? maps.a_base : maps.b_base) +
+                            (uint64_t)first * (uint64_t)(which == 0 ? maps.a_row_bytes : maps.b_row_bytes);
+      asm volatile("tensormap.replace.tile.global_address.shared::cta.b1024.b64 [%0], %1;" ::"r"(at), "l"(base)
+                   : "memory");
+      asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;" ::"r"(at), "r"(count)
+                   : "memory");
+    }
+    __syncwarp();
+    asm volatile(
+        "tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync.aligned [%0], [%1], 128;" ::"l"(
+            maps.out + m),
+        "r"(at)
+        : "memory");
+  }
 }
 
 template <int kMode>
@@ -992,9 +977,19 @@ MmPlan mm_plan(int64_t rows, int E, int J, int R, bool ragged) {
 }
 
 cudaError_t launch_mm_table(const int32_t* offsets, int E, int64_t rows, int tile_rows, const MmTable& t,
-                            WsHeader* hdr, cudaStream_t stream) {
-  const int threads = offsets == nullptr ? 32 : (E + 31) / 32 * 32;
-  return launch_pdl(mm_table_kernel, dim3(1), dim3(threads), 0, stream, offsets, E, rows, tile_rows, t, hdr);
+                            WsHeader* hdr, const MmWgradOperands* w, cudaStream_t stream) {
+  MmSegMaps maps{};
+  if (w != nullptr) {
+    if (make_tma_16(&maps.a, w->a, w->I, rows, 1, kBK) != 0 || make_tma_16(&maps.b, w->b, w->J, rows, 1, kBK) != 0)
+      return cudaErrorInvalidValue;
+    maps.a_base = w->a;
+    maps.b_base = w->b;
+    maps.a_row_bytes = (int64_t)w->I * 2;
+    maps.b_row_bytes = (int64_t)w->J * 2;
+    maps.out = t.maps;
+  }
+  const int threads = offsets == nullptr ? 32 : w != nullptr ? kMaxGroups : (E + 31) / 32 * 32;
+  return launch_pdl(mm_table_kernel, dim3(1), dim3(threads), 0, stream, offsets, E, rows, tile_rows, t, hdr, maps);
 }
 
 cudaError_t launch_mm(int mode, const void* a, const void* b, const MmArgs& m, cudaStream_t stream) {

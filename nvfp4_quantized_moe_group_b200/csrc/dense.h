@@ -25,11 +25,27 @@ enum : int { kMmForward = 0, kMmDgrad = 1, kMmWgrad = 2 };
 struct MmTable {
   int32_t* seg;          // [E][2] first row, number of rows
   int32_t* tiles;        // [E + 1] row tiles before each segment
+  CUtensorMap* maps;     // [E][2] wgrad's operands, rows of one segment (nullptr: not wanted)
+};
+
+// The operands of a ragged wgrad: A = dy [rows][I], B = x [rows][J].
+struct MmWgradOperands {
+  const void *a, *b;
+  int I, J;
+};
+
+// What the table kernel builds the segments' maps from.
+struct MmSegMaps {
+  CUtensorMap a, b;      // of the whole operands
+  const void *a_base, *b_base;
+  int64_t a_row_bytes, b_row_bytes;
+  CUtensorMap* out;      // nullptr: none
 };
 
 struct MmArgs {
   const int32_t* seg;    // as in MmTable; nullptr: one segment, all `rows` rows
   const int32_t* tiles;
+  const CUtensorMap* seg_maps;   // as MmTable.maps; nullptr with one segment
   int E;
   int64_t rows;          // token rows of the tensors
   int I;                 // kMmWgrad: rows of one expert's output
@@ -56,9 +72,10 @@ MmPlan mm_plan(int64_t rows, int E, int J, int R, bool ragged);
 
 // Zeroes the status word and the work counters and, with offsets, checks them and writes the segment table for row
 // tiles of tile_rows.  Offsets that decrease or leave 0 .. rows raise kStatusBadInput and leave
-// every segment empty, so no later kernel of the call reads or writes through them.
+// every segment empty, so no later kernel of the call reads or writes through them.  w: also the
+// segments' tensor maps for wgrad (rows > 0).
 cudaError_t launch_mm_table(const int32_t* offsets, int E, int64_t rows, int tile_rows, const MmTable& t,
-                            WsHeader* hdr, cudaStream_t stream);
+                            WsHeader* hdr, const MmWgradOperands* w, cudaStream_t stream);
 // The product.  a, b: the operands' base addresses.
 cudaError_t launch_mm(int mode, const void* a, const void* b, const MmArgs& m, cudaStream_t stream);
 
