@@ -19,8 +19,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kCols = 256;               // columns of one CTA
 
-__global__ void __launch_bounds__(kThreads) act_grad_kernel(const uint16_t* dy, const uint16_t* z, int64_t M, int N,
-                                                            int act, int fp16, uint16_t* dz, float* partials,
+__global__ void __launch_bounds__(kThreads) act_grad_kernel(const uint16_t* __restrict__ dy, const uint16_t* __restrict__ z, int64_t M, int N,
+                                                            int act, int fp16, uint16_t* __restrict__ dz, float* __restrict__ partials,
                                                             int64_t rows_per_block) {
   __shared__ float s_sum[8][kCols + 4];
   pdl_wait();
@@ -31,6 +31,7 @@ __global__ void __launch_bounds__(kThreads) act_grad_kernel(const uint16_t* dy, 
   const int64_t r1 = r0 + rows_per_block < M ? r0 + rows_per_block : M;
   float sum[8] = {};
   if (col < N) {
+#pragma unroll 2
     for (int64_t r = r0 + warp; r < r1; r += 8) {
       const int64_t at = r * N + col;
       const uint4 d4 = *reinterpret_cast<const uint4*>(dy + at);
@@ -72,13 +73,23 @@ __global__ void __launch_bounds__(kThreads) act_grad_kernel(const uint16_t* dy, 
   }
 }
 
+// Adds n rows of partial sums: 32 columns a CTA, 8 slices of the rows side by side.
 __global__ void __launch_bounds__(kThreads) sum_partials_kernel(const float* partials, int n, int N, float* out) {
+  __shared__ float s[8][33];
   pdl_wait();
   pdl_trigger();
-  const int c = blockIdx.x * kThreads + threadIdx.x;
-  if (c >= N) return;
+  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
   float t = 0.0f;
-  for (int i = 0; i < n; ++i) t += partials[(int64_t)i * N + c];
+  if (c < N) {
+#pragma unroll 4
+    for (int i = slice; i < n; i += 8) t += partials[(int64_t)i * N + c];
+  }
+  s[slice][lane] = t;
+  __syncthreads();
+  if (slice != 0 || c >= N) return;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) t += s[i][lane];
   out[c] = t;
 }
 
@@ -103,7 +114,7 @@ cudaError_t launch_act_grad(const void* dy, const void* z, int64_t M, int N, int
   if (e != cudaSuccess) return e;
   ++*launches;
   if (db == nullptr) return cudaSuccess;
-  e = launch_pdl(sum_partials_kernel, dim3((N + kThreads - 1) / kThreads), dim3(kThreads), 0, stream,
+  e = launch_pdl(sum_partials_kernel, dim3((N + 31) / 32), dim3(kThreads), 0, stream,
                  (const float*)partials, n, N, db);
   if (e == cudaSuccess) ++*launches;
   return e;

@@ -448,12 +448,15 @@ MmArgs product_args(const ProductWs& p, bool ragged, int E, int64_t M, int32_t d
   m.rows = M;
   m.fp16 = dtype == NVFP4MOE_FP16;
   m.status = &p.hdr->status;
-  m.work_counter = &p.hdr->work[0];
+  m.work_counter = ragged ? &p.hdr->work[0] : nullptr;
+  // a dense product needs nothing of the kernel that resets the status word
+  m.late_wait = !ragged;
   return m;
 }
 
-// dx = dy W (per segment) and dw = dy^T x, either of them when asked for.
-cudaError_t product_gradients(const MmArgs& base, const void* dy, const void* x, const void* w, int32_t K, int32_t N,
+// dx = dy W (per segment) and dw = dy^T x, either of them when asked for.  base.late_wait: for the
+// first of them; the second never depends on the first.
+cudaError_t product_gradients(const ProductWs& p, const MmArgs& base, const void* dy, const void* x, const void* w, int32_t K, int32_t N,
                               void* dx, void* dw, int32_t dw_dtype, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   if (dx != nullptr && base.rows > 0) {
@@ -473,7 +476,8 @@ cudaError_t product_gradients(const MmArgs& base, const void* dy, const void* x,
     m.J = K;
     m.out = dw;
     m.out_f32 = dw_dtype == NVFP4MOE_FP32;
-    m.work_counter = base.work_counter + 1;
+    m.work_counter = &p.hdr->work[1];
+    m.late_wait = base.late_wait || dx != nullptr;
     e = launch_mm(kMmWgrad, dy, x, m, s);
     if (e == cudaSuccess) ++g_launches;
   }
@@ -1726,7 +1730,7 @@ int nvfp4moe_grouped_mm_backward(int32_t dtype, const void* dy, const void* x, c
   const MmWgradOperands wgrad{dy, x, N, K};
   if (start_product(p, offsets, E, M, K, N, dw != nullptr && M > 0 ? &wgrad : nullptr, s) != cudaSuccess)
     return cuda_failed();
-  if (product_gradients(product_args(p, true, E, M, dtype), dy, x, w, K, N, dx, dw, dw_dtype, s) != cudaSuccess)
+  if (product_gradients(p, product_args(p, true, E, M, dtype), dy, x, w, K, N, dx, dw, dw_dtype, s) != cudaSuccess)
     return cuda_failed();
   return NVFP4MOE_OK;
 }
@@ -1796,8 +1800,10 @@ int nvfp4moe_linear_backward(int32_t dtype, const void* dy, const void* x, const
       return cuda_failed();
   }
   const void* dz = act != NVFP4MOE_ACT_NONE ? p.dz : dy;
-  if (product_gradients(product_args(p, false, 1, M, dtype), dz, x, w, K, N, dx, dw, dw_dtype, s) != cudaSuccess)
-    return cuda_failed();
+  MmArgs m = product_args(p, false, 1, M, dtype);
+  // with db the kernel before is the sum of its partials, which dz's has finished before
+  m.late_wait = act == NVFP4MOE_ACT_NONE || db != nullptr;
+  if (product_gradients(p, m, dz, x, w, K, N, dx, dw, dw_dtype, s) != cudaSuccess) return cuda_failed();
   return NVFP4MOE_OK;
 }
 

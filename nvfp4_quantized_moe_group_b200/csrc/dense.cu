@@ -353,11 +353,12 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
-  pdl_wait();
+  if (!p.late_wait) pdl_wait();
   pdl_trigger();
 
   const uint32_t tmem = s.tmem_base;
-  const int total = total_tiles<kMode>(p, kPairTile, kPairTile);
+  const int tile_i = kTokens ? p.tile_rows : kPairTile;
+  const int total = total_tiles<kMode>(p, tile_i, kPairTile);
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
   if (warp == 0) {
@@ -378,7 +379,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
           }
           w = next < total ? next : -1;
           // the one after it, under way while this one's loads are issued
-          if (w >= 0) next = pairs + atomicAdd(p.work_counter, 1);
+          if (w >= 0) next = p.work_counter != nullptr ? pairs + atomicAdd(p.work_counter, 1) : next + pairs;
           store_rank(&s.work[slot], &s.work_full[slot], 1, w);
           s.work[slot] = w;
           mbar_arrive(&s.work_full[slot]);
@@ -391,7 +392,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
           }
         }
         if (w < 0) break;
-        const Tile t = tile_at<kMode>(p, w, kPairTile, kPairTile);
+        const Tile t = tile_at<kMode>(p, w, tile_i, kPairTile);
         // wgrad: 128 rows of each operand; else 128 features, and half of the tile's token rows in
         // the smallest box that covers them
         const int half = kTokens ? pair_columns(t.rows_valid) / 2 : kHalf;
@@ -454,7 +455,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
           if (w == -2) set_abort(&s.abort_flag, p.status);
           break;
         }
-        const Tile t = tile_at<kMode>(p, w, kPairTile, kPairTile);
+        const Tile t = tile_at<kMode>(p, w, tile_i, kPairTile);
         if (t.steps == 0) continue;
         const uint32_t idesc =
             idesc_f16(2 * kHalf, kTokens ? pair_columns(t.rows_valid) : kPairTile, p.fp16 != 0, kAMn, kBMn);
@@ -503,7 +504,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         if (w == -2) set_abort(&s.abort_flag, p.status);
         break;
       }
-      const Tile t = tile_at<kMode>(p, w, kPairTile, kPairTile);
+      const Tile t = tile_at<kMode>(p, w, tile_i, kPairTile);
       const bool has_acc = t.steps > 0;
       if (has_acc) {
         const bool got = wait_cluster(&s.acc_full[it & 1], (uint32_t)(it >> 1) & 1u, &s.abort_flag);
@@ -566,6 +567,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
   cluster_sync();
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
+  if (p.late_wait) pdl_wait();
 }
 
 // ------------------------------------------------------------- few rows ----
@@ -578,7 +580,12 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
 // in distributed shared memory and each CTA sums and stores some of the token rows, in rank order
 // (a fixed order of additions, no workspace).
 constexpr int kNarrowThreads = 256;
-constexpr int kMaxSplit = 8;
+constexpr int kMaxSplit = 6;
+// Clusters of `split` such CTAs (one an SM) that fit a B200 at once: a cluster stays inside a GPC, so
+// fewer than 148 / split.  More would run as a second wave.
+__host__ __device__ constexpr int clusters_that_fit(int split) {
+  return split == 1 ? 148 : split == 2 ? 74 : split == 3 ? 44 : split == 4 ? 32 : split == 5 ? 25 : 21;
+}
 
 template <int kTok>
 struct NarrowCfg {
@@ -669,7 +676,7 @@ mm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
   tc_fence_before();
   if (split > 1) cluster_sync(); else __syncthreads();
   tc_fence_after();
-  pdl_wait();
+  if (!p.late_wait) pdl_wait();
   pdl_trigger();
 
   const uint32_t tmem = s.tmem_base;
@@ -818,6 +825,7 @@ mm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
   if (split > 1) cluster_sync(); else __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
+  if (p.late_wait) pdl_wait();
 }
 
 // One thread per expert: its segment from the offsets, and the scan of the row tiles; then, for wgrad,
@@ -828,10 +836,21 @@ __global__ void __launch_bounds__(kMaxGroups) mm_table_kernel(const int32_t* off
   __shared__ int warp_sum[32];
   __shared__ __align__(128) uint32_t s_map[32][32];
   pdl_wait();
-  pdl_trigger();
   const int e = threadIdx.x, lane = e & 31, warp = e >> 5;
+  if (offsets == nullptr) {
+    // a dense product may run beside this kernel: it starts after these stores
+    if (e == 0) {
+      hdr->status = 0u;
+      hdr->work[0] = hdr->work[1] = 0;
+      __threadfence();
+    }
+    __syncwarp();
+    pdl_trigger();
+    return;
+  }
+  pdl_trigger();
   int64_t lo = 0, hi = 0;
-  if (offsets != nullptr && e < E) {
+  if (e < E) {
     lo = offsets[e];
     hi = offsets[e + 1];
   }
@@ -840,7 +859,6 @@ __global__ void __launch_bounds__(kMaxGroups) mm_table_kernel(const int32_t* off
     hdr->status = bad ? kStatusBadInput : 0u;
     hdr->work[0] = hdr->work[1] = 0;
   }
-  if (offsets == nullptr) return;
   if (bad) lo = hi = 0;
   const int n = (int)((hi - lo + tile_rows - 1) / tile_rows);
   int sum = n;
@@ -887,7 +905,9 @@ __global__ void __launch_bounds__(kMaxGroups) mm_table_kernel(const int32_t* off
 }
 
 template <int kMode>
-cudaError_t launch_pair(const void* a, const void* b, const MmArgs& m, cudaStream_t stream) {
+cudaError_t launch_pair(const void* a, const void* b, const MmArgs& args, int tile_rows, cudaStream_t stream) {
+  MmArgs m = args;
+  m.tile_rows = tile_rows;
   CUtensorMap map_a, map_b, map_b64, map_b32, map_out;
   int err;
   if (kMode == kMmWgrad) {
@@ -908,7 +928,7 @@ cudaError_t launch_pair(const void* a, const void* b, const MmArgs& m, cudaStrea
   if (ce != cudaSuccess) return ce;
   const int64_t ntj = (m.J + kPairTile - 1) / kPairTile;
   int64_t most = kMode == kMmWgrad ? (int64_t)m.E * ((m.I + kPairTile - 1) / kPairTile)
-                                   : (m.rows + kPairTile - 1) / kPairTile + (m.seg != nullptr ? m.E : 0);
+                                   : (m.rows + tile_rows - 1) / tile_rows + (m.seg != nullptr ? m.E : 0);
   most *= ntj;
   const int64_t pairs = num_sms() / 2;
   return launch_pdl(mm_pair_kernel<kMode>, dim3((unsigned)(2 * (most < pairs ? most : pairs))), dim3(kPairThreads),
@@ -930,7 +950,7 @@ cudaError_t launch_narrow(const void* a, const void* b, const MmArgs& m, int spl
   int64_t most = (m.rows + kTok - 1) / kTok;
   if (m.seg != nullptr) most += m.E < m.rows ? m.E : m.rows;
   most *= (m.J + kHalf - 1) / kHalf;
-  const int64_t room = num_sms() / split;
+  const int64_t room = clusters_that_fit(split);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((most < room ? most : room) * split));
   cfg.blockDim = dim3(kNarrowThreads);
@@ -951,29 +971,53 @@ cudaError_t launch_narrow(const void* a, const void* b, const MmArgs& m, int spl
 template <int kMode>
 cudaError_t launch_rows(const void* a, const void* b, const MmArgs& m, cudaStream_t stream) {
   const MmPlan plan = mm_plan(m.rows, m.E, m.J, m.R, m.seg != nullptr);
+  if (plan.pair) return launch_pair<kMode>(a, b, m, plan.tile_rows, stream);
   switch (plan.tile_rows) {
     case 16: return launch_narrow<kMode, 16>(a, b, m, plan.split, stream);
     case 32: return launch_narrow<kMode, 32>(a, b, m, plan.split, stream);
     case 64: return launch_narrow<kMode, 64>(a, b, m, plan.split, stream);
-    case 128: return launch_narrow<kMode, 128>(a, b, m, plan.split, stream);
-    default: return launch_pair<kMode>(a, b, m, stream);
+    default: return launch_narrow<kMode, 128>(a, b, m, plan.split, stream);
   }
 }
 
 }  // namespace
 
+// The cheapest of the shapes by a model in SM clocks.  A tile's step takes the time to bring its
+// operands in (about 45 bytes a clock and SM, latency included) or the tensor time; waves of tiles follow one
+// another; and nothing is faster than the weights from HBM (3500 bytes a clock).  Measured at K = N =
+// 5120: 16 rows 11.0 us on single CTAs split 3 ways, 18.6 on pairs; 128 rows 17.1 and 20.5; 384 rows
+// 27.4 and 24.5; 16 experts of 96 rows 93.3 and 90.4, of 192 rows 122 and 100.
 MmPlan mm_plan(int64_t rows, int E, int J, int R, bool ragged) {
-  MmPlan plan{kPairTile, 1};
-  const int64_t mean = (rows + E - 1) / E;     // the split among the experts is known on the device only
-  if (mean > 128) return plan;
-  plan.tile_rows = mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 ? 64 : 128;
-  const int64_t row_tiles = ragged ? (E < rows ? E : rows) : (rows + plan.tile_rows - 1) / plan.tile_rows;
-  const int64_t tiles = row_tiles * ((J + kHalf - 1) / kHalf);
   const int64_t steps = (R + kBK - 1) / kBK;
-  int64_t split = tiles > 0 ? 148 / tiles : 1;
-  if (split > steps / 4) split = steps / 4;
-  plan.split = (int)(split < 1 ? 1 : split > kMaxSplit ? kMaxSplit : split);
-  return plan;
+  // how the rows spread over the experts is known on the device only: evenly, for the model
+  const int64_t busy = ragged ? (E < rows ? E : rows) : 1;
+  const int64_t mean = busy > 0 ? (rows + busy - 1) / busy : 0;
+  MmPlan best{false, 16, 1};
+  if (mean == 0) return best;
+  const double hbm = (double)busy * J * R * 2.0 / 3500.0;
+  double best_cost = 1e30;
+  auto consider = [&](bool pair, int tile, int split) {
+    const int64_t per_seg = (mean + tile - 1) / tile, cols = pair ? kPairTile : kHalf;
+    const int64_t tiles = busy * per_seg * ((J + cols - 1) / cols);
+    const int64_t room = pair ? 74 : clusters_that_fit(split);
+    const int64_t waves = (tiles + room - 1) / room;
+    const double n = pair ? (double)(((mean + per_seg - 1) / per_seg + 31) / 32 * 32) : (double)tile;
+    double step = (16384.0 + (pair ? 64.0 : 128.0) * n) / 45.0;
+    if (step < 2.0 * n) step = 2.0 * n;
+    double cost = (double)waves * (double)((steps + split - 1) / split) * step;
+    if (cost < hbm) cost = hbm;
+    cost += pair ? 4000.0 + 12.0 * n : 2500.0 + 25.0 * n + (split > 1 ? (600.0 + 8.0 * n) * (double)waves : 0.0);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = MmPlan{pair, tile, split};
+    }
+  };
+  for (int tile = 16; tile <= 128; tile *= 2) {
+    if (tile >= 32 && mean <= tile / 2) break;               // all padding
+    for (int split = 1; split <= kMaxSplit && split * 4 <= (steps > 4 ? steps : 4); ++split) consider(false, tile, split);
+  }
+  for (int tile = kPairTile; tile >= 64; tile -= 32) consider(true, tile, 1);
+  return best;
 }
 
 cudaError_t launch_mm_table(const int32_t* offsets, int E, int64_t rows, int tile_rows, const MmTable& t,
@@ -996,7 +1040,7 @@ cudaError_t launch_mm(int mode, const void* a, const void* b, const MmArgs& m, c
   switch (mode) {
     case kMmForward: return launch_rows<kMmForward>(a, b, m, stream);
     case kMmDgrad: return launch_rows<kMmDgrad>(a, b, m, stream);
-    default: return launch_pair<kMmWgrad>(a, b, m, stream);
+    default: return launch_pair<kMmWgrad>(a, b, m, kPairTile, stream);
   }
 }
 

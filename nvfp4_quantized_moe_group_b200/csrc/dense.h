@@ -59,12 +59,19 @@ struct MmArgs {
   const void* residual;  // [rows][J] or nullptr, the operands' type
   void* z_out;           // [rows][J] or nullptr: the sums with the bias, before the activation
   uint32_t* status;
-  int* work_counter;     // zero at launch: tiles handed out beyond the first of each CTA pair
+  int late_wait;         // the previous kernel of the stream is not one this product depends on, and has
+                         // itself waited for those it does: it may run beside that kernel, and waits
+                         // for it only before it ends (so that the kernel after it can wait for both)
+  int* work_counter;     // pairs; zero at launch: tiles handed out beyond the first of each CTA pair
+                         // (nullptr: fixed turns, for tiles of one cost)
+  int tile_rows;         // pairs: most token rows of a tile (set by launch_mm)
 };
 
-// How forward and dgrad run: token rows of a tile (16 to 128: one CTA a tile, `split` CTAs share its
-// reduction; 256: CTA pairs).  J output columns, R the reduction length.
+// How forward and dgrad run: on CTA pairs with tiles of up to tile_rows token rows (a multiple of 32 up
+// to 256), or on single CTAs with tiles of tile_rows (16, 32, 64, 128), `split` CTAs sharing a tile's
+// reduction.  J output columns, R the reduction length.
 struct MmPlan {
+  bool pair;
   int tile_rows;
   int split;
 };

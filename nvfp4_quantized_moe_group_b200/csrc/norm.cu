@@ -552,8 +552,10 @@ __global__ void __launch_bounds__(256) norm_param_sum_kernel(const float* partia
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;              // column of [dgamma | dbeta]
   float t = 0.0f;
-  if (c < 2 * cols)
+  if (c < 2 * cols) {
+#pragma unroll 8
     for (int i = slice; i < parts; i += 8) t += partials[(int64_t)i * 2 * cols + c];
+  }
   s[slice][lane] = t;
   __syncthreads();
   if (slice != 0 || c >= 2 * cols) return;
