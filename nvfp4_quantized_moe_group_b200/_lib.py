@@ -8,6 +8,7 @@ Loading fails loudly when the library is missing: there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
@@ -197,7 +198,7 @@ def _check(status: int, what: str):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _require(*specs):
@@ -213,18 +214,21 @@ def _require(*specs):
             raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
         if t.dtype != dtype:
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if shape is not None and tuple(t.shape) != tuple(int(s) for s in shape):
+        if shape is not None and t.shape != shape:
             raise TypeError(f"{name} must have shape {tuple(int(s) for s in shape)}, got {tuple(t.shape)}")
         if not t.is_contiguous():
             raise TypeError(f"{name} must be contiguous")
+    if not present:
+        return
+    device = present[0][0].device
     for t, name, _, _ in present:
-        if not t.is_cuda or t.device != present[0][0].device:
-            raise TypeError(f"{name} must be a CUDA tensor on {present[0][0].device}, got {t.device}")
+        if not t.is_cuda or t.device != device:
+            raise TypeError(f"{name} must be a CUDA tensor on {device}, got {t.device}")
     # the library launches on the current device: tensors of another one would be read
     # through addresses that device does not map
-    if present and present[0][0].device.index != torch.cuda.current_device():
-        raise TypeError(f"the tensors are on {present[0][0].device} but the current device is "
-                        f"cuda:{torch.cuda.current_device()}: call under torch.cuda.device({present[0][0].device})")
+    if device.index != torch.cuda.current_device():
+        raise TypeError(f"the tensors are on {device} but the current device is "
+                        f"cuda:{torch.cuda.current_device()}: call under torch.cuda.device({device})")
 
 
 def _rows(x, name: str, min_rows: int = 1) -> int:
@@ -242,8 +246,10 @@ def _layer_specs(cfg, x, w_router, bias, name="x") -> list:
 
 
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    # the handle alone: building a torch.cuda.Stream object costs more than a small kernel's launch
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _workspace(nbytes: int, device) -> torch.Tensor:
@@ -831,6 +837,7 @@ def _dw_dtype(dw_dtype, dt) -> torch.dtype:
     return dw_dtype
 
 
+@functools.lru_cache(maxsize=1024)
 def grouped_mm_workspace_bytes(E: int) -> int:
     return int(lib().nvfp4moe_grouped_mm_workspace_bytes(int(E)))
 
@@ -885,6 +892,7 @@ def grouped_mm_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, offs
     return dx, dw
 
 
+@functools.lru_cache(maxsize=1024)
 def linear_workspace_bytes(M: int, K: int, N: int) -> int:
     return int(lib().nvfp4moe_linear_workspace_bytes(int(M), int(K), int(N)))
 
@@ -913,6 +921,7 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None, a
     return (out, z) if save_z else out
 
 
+@functools.lru_cache(maxsize=1024)
 def linear_backward_workspace_bytes(M: int, K: int, N: int) -> int:
     return int(lib().nvfp4moe_linear_backward_workspace_bytes(int(M), int(K), int(N)))
 
@@ -969,6 +978,7 @@ def layer_norm(x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.T
     return (out, mean, rstd) if stats else out
 
 
+@functools.lru_cache(maxsize=1024)
 def layer_norm_backward_workspace_bytes(rows: int, cols: int) -> int:
     return int(lib().nvfp4moe_layer_norm_backward_workspace_bytes(int(rows), int(cols)))
 

@@ -6,7 +6,8 @@
 // pass.  A CTA owns 256 columns (32 lanes x 8) and a block of rows; its 8 warps take rows in turn
 // and add their columns in registers, the warps' sums are added in shared memory and one row of
 // partial sums per row block goes to the workspace; a second kernel adds those in a fixed order,
-// so db does not depend on how the CTAs ran.
+// so db does not depend on how the CTAs ran.  The first kernel of its call, it also resets the
+// workspace's status word and work counters.
 #include "activation.cuh"
 #include "common.cuh"
 #include "dense.h"
@@ -19,12 +20,16 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kCols = 256;               // columns of one CTA
 
-__global__ void __launch_bounds__(kThreads) act_grad_kernel(const uint16_t* __restrict__ dy, const uint16_t* __restrict__ z, int64_t M, int N,
-                                                            int act, int fp16, uint16_t* __restrict__ dz, float* __restrict__ partials,
-                                                            int64_t rows_per_block) {
+__global__ void __launch_bounds__(kThreads)
+act_grad_kernel(const uint16_t* __restrict__ dy, const uint16_t* __restrict__ z, int64_t M, int N, int act, int fp16,
+                uint16_t* __restrict__ dz, float* __restrict__ partials, int64_t rows_per_block, WsHeader* hdr) {
   __shared__ float s_sum[8][kCols + 4];
   pdl_wait();
   pdl_trigger();
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
+    hdr->status = 0u;
+    hdr->work[0] = hdr->work[1] = 0;
+  }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = blockIdx.x * kCols + lane * 8;
   const int64_t r0 = (int64_t)blockIdx.y * rows_per_block;
@@ -105,12 +110,12 @@ int act_grad_partials(int64_t M, int64_t N) {
 }
 
 cudaError_t launch_act_grad(const void* dy, const void* z, int64_t M, int N, int act, bool fp16, void* dz, float* db,
-                            float* partials, int* launches, cudaStream_t stream) {
+                            float* partials, WsHeader* hdr, int* launches, cudaStream_t stream) {
   const int n = act_grad_partials(M, N);
   const int64_t rows = (M + n - 1) / n;
   cudaError_t e = launch_pdl(act_grad_kernel, dim3((N + kCols - 1) / kCols, n), dim3(kThreads), 0, stream,
                              static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(z), M, N, act,
-                             fp16 ? 1 : 0, static_cast<uint16_t*>(dz), db != nullptr ? partials : nullptr, rows);
+                             fp16 ? 1 : 0, static_cast<uint16_t*>(dz), db != nullptr ? partials : nullptr, rows, hdr);
   if (e != cudaSuccess) return e;
   ++*launches;
   if (db == nullptr) return cudaSuccess;

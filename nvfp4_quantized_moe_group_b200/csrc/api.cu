@@ -1792,13 +1792,16 @@ int nvfp4moe_linear_backward(int32_t dtype, const void* dy, const void* x, const
   const int st = check_device();
   if (st != NVFP4MOE_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (start_product(p, nullptr, 1, M, N, K, nullptr, s) != cudaSuccess) return cuda_failed();
-  if (M == 0) {
-    if (db != nullptr && cudaMemsetAsync(db, 0, (size_t)N * sizeof(float), s) != cudaSuccess) return cuda_failed();
-  } else if (act != NVFP4MOE_ACT_NONE || db != nullptr) {
-    if (launch_act_grad(dy, z, M, N, act, dtype == NVFP4MOE_FP16, p.dz, db, p.partials, &g_launches, s) != cudaSuccess)
+  if (M > 0 && (act != NVFP4MOE_ACT_NONE || db != nullptr)) {
+    g_last_status = p.hdr;
+    if (launch_act_grad(dy, z, M, N, act, dtype == NVFP4MOE_FP16, p.dz, db, p.partials, p.hdr, &g_launches, s) !=
+        cudaSuccess)
       return cuda_failed();
+  } else if (start_product(p, nullptr, 1, M, N, K, nullptr, s) != cudaSuccess) {
+    return cuda_failed();
   }
+  if (M == 0 && db != nullptr && cudaMemsetAsync(db, 0, (size_t)N * sizeof(float), s) != cudaSuccess)
+    return cuda_failed();
   const void* dz = act != NVFP4MOE_ACT_NONE ? p.dz : dy;
   MmArgs m = product_args(p, false, 1, M, dtype);
   // with db the kernel before is the sum of its partials, which dz's has finished before

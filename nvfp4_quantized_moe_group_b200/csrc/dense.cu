@@ -924,7 +924,7 @@ cudaError_t launch_pair(const void* a, const void* b, const MmArgs& args, int ti
   if (err != 0) return cudaErrorInvalidValue;
   const size_t smem = sizeof(PairSmem) + 1024;
   static_assert(sizeof(PairSmem) + 1024 <= 232448, "shared memory exceeds the per-block limit");
-  cudaError_t ce = cudaFuncSetAttribute(mm_pair_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const cudaError_t ce = allow_smem(reinterpret_cast<const void*>(mm_pair_kernel<kMode>), smem);
   if (ce != cudaSuccess) return ce;
   const int64_t ntj = (m.J + kPairTile - 1) / kPairTile;
   int64_t most = kMode == kMmWgrad ? (int64_t)m.E * ((m.I + kPairTile - 1) / kPairTile)
@@ -945,7 +945,7 @@ cudaError_t launch_narrow(const void* a, const void* b, const MmArgs& m, int spl
   const size_t smem = sizeof(NarrowSmem<kTok>) + 1024;
   static_assert(sizeof(NarrowSmem<kTok>) + 1024 <= 232448, "shared memory exceeds the per-block limit");
   auto kernel = mm_narrow_kernel<kMode, kTok>;
-  const cudaError_t ce = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const cudaError_t ce = allow_smem(reinterpret_cast<const void*>(kernel), smem);
   if (ce != cudaSuccess) return ce;
   int64_t most = (m.rows + kTok - 1) / kTok;
   if (m.seg != nullptr) most += m.E < m.rows ? m.E : m.rows;

@@ -87,10 +87,11 @@ cudaError_t launch_mm_table(const int32_t* offsets, int E, int64_t rows, int til
 cudaError_t launch_mm(int mode, const void* a, const void* b, const MmArgs& m, cudaStream_t stream);
 
 // dz = dy act'(z) (16 bit, written when act is not NONE) and db[n] = sum_m dy act'(z) (FP32, when
-// db is not nullptr; partials: act_grad_partials(M) * N floats).
+// db is not nullptr; partials: act_grad_partials(M, N) * N floats).  Resets the workspace header as
+// launch_mm_table does.
 int act_grad_partials(int64_t M, int64_t N);
 cudaError_t launch_act_grad(const void* dy, const void* z, int64_t M, int N, int act, bool fp16, void* dz, float* db,
-                            float* partials, int* launches, cudaStream_t stream);
+                            float* partials, WsHeader* hdr, int32_t* launches, cudaStream_t stream);
 
 // gemm.cu: tensor map of 2- or 4-byte elements [batch][rows][inner], a box of 128 bytes x box_rows x 1, 128B
 // swizzle.

@@ -901,6 +901,23 @@ int make_tma_3d(CUtensorMap* map, const void* base, uint32_t elem_bytes, uint64_
   return r == CUDA_SUCCESS ? 0 : (int)r;
 }
 
+cudaError_t allow_smem(const void* kernel, size_t bytes) {
+  struct Entry {
+    const void* kernel;
+    int device;
+    size_t bytes;
+  };
+  thread_local Entry seen[64] = {};
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  Entry& at = seen[(reinterpret_cast<uintptr_t>(kernel) >> 4) % 64];
+  if (at.kernel == kernel && at.device == device && at.bytes >= bytes) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) at = Entry{kernel, device, bytes};
+  return e;
+}
+
 int num_sms() {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 148;

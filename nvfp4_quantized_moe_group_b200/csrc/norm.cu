@@ -583,7 +583,7 @@ constexpr int kFewRows = 2 * 148;
 
 template <typename Kernel>
 cudaError_t launch_norm(Kernel kernel, int grid, int threads, size_t smem, const NormArgs& a, cudaStream_t stream) {
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(kernel, dim3(grid), dim3(threads), smem, stream, a);
 }
@@ -660,7 +660,7 @@ cudaError_t backward_wide(const NormArgs& a, int ctas, cudaStream_t stream) {
   const int n_vecs = (span_of(a.cols, vec_of(kType)) + vec_of(kType) - 1) / vec_of(kType);
   const size_t smem = (size_t)n_vecs * vec_of(kType) * 2 * sizeof(float);
   const auto kernel = norm_backward_wide_kernel<kType, kAligned>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(kernel, dim3(ctas), dim3(1024), smem, stream, a, n_vecs);
 }
