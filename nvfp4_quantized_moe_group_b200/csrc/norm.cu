@@ -182,7 +182,11 @@ struct Columns {
     cp_async16(dst, static_cast<const T*>(base) + row * cols + c,
                kAligned || left >= kVec ? 16 : left * (int)sizeof(T));
   }
-  // The values of one vector; 0 outside the row.
+  // Only a row's first vector (k = 0 of the first thread) has elements in front of the row, only its last
+  // one elements behind it.
+  __device__ __forceinline__ bool head(int k) const { return !kAligned && k == 0 && col0 < 0; }
+  __device__ __forceinline__ bool tail(int k) const { return !kAligned && col(k) + kVec > cols; }
+  // The values of one vector; 0 outside the row (the copy has filled zeros behind it).
   __device__ __forceinline__ void values(const uint4& raw, int k, float* v) const {
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
@@ -195,29 +199,41 @@ struct Columns {
         v[2 * i + 1] = f.y;
       }
     }
-    clear(k, v);
+    clear_head(k, v);
+  }
+  __device__ __forceinline__ void clear_head(int k, float* v) const {
+    if (head(k)) {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) v[i] = i < lead ? 0.0f : v[i];
+    }
   }
   __device__ __forceinline__ void clear(int k, float* v) const {
-    if (!whole(k)) {
+    clear_head(k, v);
+    if (tail(k)) {
+      const int left = cols - col(k);
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) v[i] = has(k, i) ? v[i] : 0.0f;
+      for (int i = 0; i < kVec; ++i) v[i] = i < left ? v[i] : 0.0f;
     }
   }
   __device__ __forceinline__ void store(void* base, int64_t row, int k, const float* v) const {
     using T = typename Elem<kType>::T;
     T* at = static_cast<T*>(base) + row * cols + col(k);
-    if (whole(k)) {
-      uint32_t w[4];
+    uint32_t w[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (kType == NVFP4MOE_FP32) w[i] = __float_as_uint(v[i]);
-        else w[i] = pack16(v[2 * i], v[2 * i + 1], kType == NVFP4MOE_FP16);
-      }
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (kType == NVFP4MOE_FP32) w[i] = __float_as_uint(v[i]);
+      else w[i] = pack16(v[2 * i], v[2 * i + 1], kType == NVFP4MOE_FP16);
+    }
+    if (!head(k) && !tail(k)) {
       *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
+      const int from = head(k) ? lead : 0, to = tail(k) ? cols - col(k) : kVec;
 #pragma unroll
-      for (int i = 0; i < kVec; ++i)
-        if (has(k, i)) at[i] = from_f32<kType>(v[i]);
+      for (int i = 0; i < kVec; ++i) {
+        if (i < from || i >= to) continue;
+        if constexpr (kType == NVFP4MOE_FP32) at[i] = v[i];
+        else at[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+      }
     }
   }
 };
@@ -236,32 +252,38 @@ struct Ring {
   static_assert(kRows >= 1, "a row of every group fits shared memory");
 };
 
-template <int kType, bool kAligned, int kG, int kPer, int kGroups, int kParams>
+// kR rows at a time per group: the parameters' reads and the barriers serve all of them.
+template <int kType, bool kAligned, int kG, int kPer, int kGroups, int kR, int kParams>
 __global__ void __launch_bounds__(kG * kGroups, 1) norm_forward_kernel(const __grid_constant__ NormArgs a) {
-  using R = Ring<kType, kAligned, kG, kPer, kGroups, 1, kParams>;
+  using R = Ring<kType, kAligned, kG, kPer, kGroups, kR, kParams>;
   using Cols = typename R::Cols;
   constexpr int kVec = Cols::kVec, kVecs = Cols::kVecs, kRing = R::kRows, kThreads = kG * kGroups;
   extern __shared__ __align__(16) uint8_t s_dyn[];
   float* s_gamma = reinterpret_cast<float*>(s_dyn);
   float* s_beta = reinterpret_cast<float*>(s_dyn + R::kParamBytes / 2);
-  uint4* s_ring = reinterpret_cast<uint4*>(s_dyn + R::kParamBytes) + threadIdx.x;    // [kRing][kVecs][threads]
-  __shared__ float s_red[kGroups][2][kG / 32];
+  uint4* s_ring = reinterpret_cast<uint4*>(s_dyn + R::kParamBytes) + threadIdx.x;    // [kRing][kR][kVecs][threads]
+  __shared__ float s_red[kGroups][2][kR * (kG / 32)];
   pdl_wait();
   pdl_trigger();
   const int group = threadIdx.x / kG;
   const int64_t step = (int64_t)gridDim.x * kGroups;
   int64_t row = Cols::first_row(kGroups, group);
   const Cols c(a, row);
-  auto fetch = [&](int64_t r, int at) {
-    if (r < a.rows) {
+  auto slot = [&](int at, int r, int k) { return s_ring + ((at * kR + r) * kVecs + k) * kThreads; };
+  auto fetch = [&](int64_t row0, int at) {
 #pragma unroll
-      for (int k = 0; k < kVecs; ++k)
-        if (c.some(k)) c.fetch(s_ring + (at * kVecs + k) * kThreads, a.x, r, k);
+    for (int r = 0; r < kR; ++r) {
+      const int64_t from = row0 + r * step;
+      if (from < a.rows) {
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k)
+          if (c.some(k)) c.fetch(slot(at, r, k), a.x, from, k);
+      }
     }
     cp_async_commit();
   };
 #pragma unroll
-  for (int i = 0; i < kRing - 1; ++i) fetch(row + i * step, i);
+  for (int i = 0; i < kRing - 1; ++i) fetch(row + i * kR * step, i);
   const bool affine = a.gamma != nullptr || a.beta != nullptr;
   const bool vec_g = (reinterpret_cast<uintptr_t>(a.gamma) & 15) == 0;
   const bool vec_b = (reinterpret_cast<uintptr_t>(a.beta) & 15) == 0;
@@ -272,47 +294,59 @@ __global__ void __launch_bounds__(kG * kGroups, 1) norm_forward_kernel(const __g
   }
   const float inv_cols = 1.0f / (float)a.cols;
   int at = 0, turn = 0;
-  for (; row < a.rows; row += step) {
-    fetch(row + (kRing - 1) * step, at == 0 ? kRing - 1 : at - 1);
+  for (; row < a.rows; row += kR * step) {
+    fetch(row + (kRing - 1) * kR * step, at == 0 ? kRing - 1 : at - 1);
     cp_async_wait<kRing - 1>();
-    float v[kVecs][kVec];
-    float sum = 0.0f;
+    float v[kR][kVecs][kVec], mean[kR], sq[kR];
 #pragma unroll
-    for (int k = 0; k < kVecs; ++k)
-      if (c.some(k)) {
-        c.values(s_ring[(at * kVecs + k) * kThreads], k, v[k]);
+    for (int r = 0; r < kR; ++r) {
+      const bool live = r == 0 || row + r * step < a.rows;
+      mean[r] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) sum += v[k][i];
-      }
-    float mean = 0.0f;
+      for (int k = 0; k < kVecs; ++k)
+        if (live && c.some(k)) {
+          c.values(*slot(at, r, k), k, v[r][k]);
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) mean[r] += v[r][k][i];
+        }
+    }
     if (!a.rms) {
-      ring_sum<1, kG>(&sum, s_red[group][0], group);
-      mean = sum * inv_cols;
+      ring_sum<kR, kG>(mean, s_red[group][0], group);
+#pragma unroll
+      for (int r = 0; r < kR; ++r) mean[r] *= inv_cols;
+    } else {
+#pragma unroll
+      for (int r = 0; r < kR; ++r) mean[r] = 0.0f;
     }
-    float sq = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kVecs; ++k)
-      if (c.some(k)) {
+    for (int r = 0; r < kR; ++r) {
+      const bool live = r == 0 || row + r * step < a.rows;
+      sq[r] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) v[k][i] -= mean;
-        c.clear(k, v[k]);
+      for (int k = 0; k < kVecs; ++k)
+        if (live && c.some(k)) {
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) sq = fmaf(v[k][i], v[k][i], sq);
+          for (int i = 0; i < kVec; ++i) v[r][k][i] -= mean[r];
+          c.clear(k, v[r][k]);
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) sq[r] = fmaf(v[r][k][i], v[r][k][i], sq[r]);
+        }
+    }
+    ring_sum<kR, kG>(sq, s_red[group][a.rms ? turn : 1], group);
+    float rstd[kR];
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      rstd[r] = rsqrtf(fmaf(sq[r], inv_cols, a.eps));
+      if (threadIdx.x % kG == 0 && (r == 0 || row + r * step < a.rows)) {
+        if (a.mean != nullptr) a.mean[row + r * step] = mean[r];
+        if (a.rstd != nullptr) a.rstd[row + r * step] = rstd[r];
       }
-    ring_sum<1, kG>(&sq, s_red[group][a.rms ? turn : 1], group);
-    const float rstd = rsqrtf(fmaf(sq, inv_cols, a.eps));
-    if (threadIdx.x % kG == 0) {
-      if (a.mean != nullptr) a.mean[row] = mean;
-      if (a.rstd != nullptr) a.rstd[row] = rstd;
     }
 #pragma unroll
     for (int k = 0; k < kVecs; ++k)
       if (c.some(k)) {
-        if (!affine) {
-#pragma unroll
-          for (int i = 0; i < kVec; ++i) v[k][i] *= rstd;
-        } else {
-          float g[kVec], b[kVec];
+        float g[kVec], b[kVec];
+        if (affine) {
           if (kParams > 0) {
             c.params(s_gamma, k, g);
             c.params(s_beta, k, b);
@@ -320,10 +354,18 @@ __global__ void __launch_bounds__(kG * kGroups, 1) norm_forward_kernel(const __g
             c.params_global(a.gamma, vec_g, 1.0f, k, g);
             c.params_global(a.beta, vec_b, 0.0f, k, b);
           }
-#pragma unroll
-          for (int i = 0; i < kVec; ++i) v[k][i] = fmaf(v[k][i] * rstd, g[i], b[i]);
         }
-        c.store(a.y, row, k, v[k]);
+#pragma unroll
+        for (int r = 0; r < kR; ++r)
+          if (r == 0 || row + r * step < a.rows) {
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) v[r][k][i] *= rstd[r];
+            if (affine) {
+#pragma unroll
+              for (int i = 0; i < kVec; ++i) v[r][k][i] = fmaf(v[r][k][i], g[i], b[i]);
+            }
+            c.store(a.y, row + r * step, k, v[r][k]);
+          }
       }
     at = at == kRing - 1 ? 0 : at + 1;
     turn ^= 1;
@@ -592,30 +634,34 @@ int vec_of(int dtype) { return dtype == NVFP4MOE_FP32 ? 4 : 8; }
 // Columns that a row may span counted from an aligned vector's start.
 int span_of(int cols, int vec) { return cols % vec == 0 ? cols : cols + vec - 1; }
 
-// Shapes by row width: threads of a group x elements a thread, and groups per CTA.  Forward runs up to 896
-// threads an SM (72 registers), backward up to 512 (the column sums take 64 registers more); FP32 rows,
-// twice the bytes for the same instructions, take half the groups, so that the rings stay deep.
-template <int kType, bool kAligned, int kG, int kPer, int kGroups16, int kParams>
+// Shapes by row width: threads of a group x elements a thread, and groups per CTA, 512 threads an SM
+// (forward works on two 16-bit rows at a time, backward holds the column sums: both about 128
+// registers).  FP32 rows, twice the bytes for the same instructions, go one at a time, and backward takes
+// half the groups, so that the rings stay deep.
+template <int kType, bool kAligned, int kG, int kPer, int kGroups, int kParams>
 cudaError_t forward_go(const NormArgs& a, cudaStream_t stream) {
-  constexpr int kGroups = kType == NVFP4MOE_FP32 ? (kGroups16 + 1) / 2 : kGroups16;
   if (a.rows <= kFewRows)
-    return launch_norm(norm_forward_kernel<kType, kAligned, kG, kPer, 1, 0>, grid_of(a.rows, 1, kAligned), kG,
+    return launch_norm(norm_forward_kernel<kType, kAligned, kG, kPer, 1, 1, 0>, grid_of(a.rows, 1, kAligned), kG,
                        Ring<kType, kAligned, kG, kPer, 1, 1, 0>::kBytes, a, stream);
-  return launch_norm(norm_forward_kernel<kType, kAligned, kG, kPer, kGroups, kParams>,
+  // wide rows that start inside vectors: the parameters shifted in shared memory, and one row at a time
+  constexpr int kR = kType == NVFP4MOE_FP32 || kG > 512 || (kG == 512 && !kAligned) ? 1 : 2;
+  return launch_norm(norm_forward_kernel<kType, kAligned, kG, kPer, kGroups, kR, kParams>,
                      grid_of(a.rows, kGroups, kAligned), kG * kGroups,
-                     Ring<kType, kAligned, kG, kPer, kGroups, 1, kParams>::kBytes, a, stream);
+                     Ring<kType, kAligned, kG, kPer, kGroups, kR, kParams>::kBytes, a, stream);
 }
 
 template <int kType, bool kAligned>
 cudaError_t forward_ring(const NormArgs& a, cudaStream_t stream) {
   const int span = span_of(a.cols, vec_of(kType));
-  if (span <= 256) return forward_go<kType, kAligned, 32, 8, 28, 2>(a, stream);
-  if (span <= 1024) return forward_go<kType, kAligned, 32, 32, 28, 2>(a, stream);
-  if (span <= 2048) return forward_go<kType, kAligned, 64, 32, 14, 2>(a, stream);
-  if (span <= 4096) return forward_go<kType, kAligned, 128, 32, 7, 2>(a, stream);
-  if (span <= 5120) return forward_go<kType, kAligned, 160, 32, 5, 2>(a, stream);
-  if (span <= 8192) return forward_go<kType, kAligned, 256, 32, 3, 2>(a, stream);
-  if (span <= 16384) return forward_go<kType, kAligned, 512, 32, 2, 0>(a, stream);
+  if (span <= 256) return forward_go<kType, kAligned, 32, 8, 16, 2>(a, stream);
+  if (span <= 1024) return forward_go<kType, kAligned, 32, 32, 16, 2>(a, stream);
+  if (span <= 2048) return forward_go<kType, kAligned, 64, 32, 8, 2>(a, stream);
+  if (span <= 3064) return forward_go<kType, kAligned, 96, 32, 5, 2>(a, stream);
+  if (span <= 4096) return forward_go<kType, kAligned, 128, 32, 4, 2>(a, stream);
+  if (span <= 5120) return forward_go<kType, kAligned, 160, 32, 3, 2>(a, stream);
+  if (span <= 6144) return forward_go<kType, kAligned, 192, 32, 2, 2>(a, stream);
+  if (span <= 8192) return forward_go<kType, kAligned, 256, 32, 2, 2>(a, stream);
+  if (span <= 16384) return forward_go<kType, kAligned, 512, 32, 1, kAligned ? 0 : 2>(a, stream);
   return forward_go<kType, kAligned, 928, 32, 1, 0>(a, stream);
 }
 
@@ -623,7 +669,8 @@ cudaError_t forward_ring(const NormArgs& a, cudaStream_t stream) {
 constexpr int kBackwardWidest = 16384;
 constexpr int backward_groups(int g16, bool f32) { return f32 ? (g16 + 1) / 2 : g16; }
 int backward_groups_of(int span, bool f32) {
-  const int g16 = span <= 1024 ? 16 : span <= 2048 ? 8 : span <= 4096 ? 4 : span <= 5120 ? 3 : span <= 8192 ? 2 : 1;
+  const int g16 = span <= 1024 ? 16 : span <= 2048 ? 8 : span <= 3064 ? 5 : span <= 4096 ? 4 : span <= 5120 ? 3
+                  : span <= 8192 ? 2 : 1;
   return backward_groups(g16, f32);
 }
 
@@ -643,8 +690,10 @@ cudaError_t backward_ring(const NormArgs& a, int ctas, cudaStream_t stream) {
   if (span <= 256) return backward_go<kType, kAligned, 32, 8, 16>(a, ctas, stream);
   if (span <= 1024) return backward_go<kType, kAligned, 32, 32, 16>(a, ctas, stream);
   if (span <= 2048) return backward_go<kType, kAligned, 64, 32, 8>(a, ctas, stream);
+  if (span <= 3064) return backward_go<kType, kAligned, 96, 32, 5>(a, ctas, stream);
   if (span <= 4096) return backward_go<kType, kAligned, 128, 32, 4>(a, ctas, stream);
   if (span <= 5120) return backward_go<kType, kAligned, 160, 32, 3>(a, ctas, stream);
+  if (span <= 6144) return backward_go<kType, kAligned, 192, 32, 2>(a, ctas, stream);
   if (span <= 8192) return backward_go<kType, kAligned, 256, 32, 2>(a, ctas, stream);
   return backward_go<kType, kAligned, 512, 32, 1>(a, ctas, stream);
 }
