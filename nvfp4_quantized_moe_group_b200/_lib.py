@@ -823,6 +823,15 @@ def _dtype_of(t, name: str, allowed) -> torch.dtype:
 _HALF = (torch.bfloat16, torch.float16)
 
 
+def _keep(stream, *tensors):
+    """Outputs and workspaces come from the current stream's allocator: on another stream they stay
+    reserved until that stream has passed the call, also when the caller drops them before."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
 def _activation(act: str) -> int:
     if act not in ACTIVATIONS:
         raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}, got {act!r}")
@@ -861,6 +870,7 @@ def grouped_mm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, out: tor
         ws = _workspace(grouped_mm_workspace_bytes(E), x.device)
     _check(lib().nvfp4moe_grouped_mm(DTYPES[dt], _ptr(x), M, K, _ptr(w), E, N, _ptr(offsets), _ptr(out), _ptr(ws),
                                      ws.numel(), _stream(stream)), "nvfp4moe_grouped_mm")
+    _keep(stream, out, ws)
     return out
 
 
@@ -889,6 +899,7 @@ def grouped_mm_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, offs
     _check(lib().nvfp4moe_grouped_mm_backward(DTYPES[dt], _ptr(dy), _ptr(x), _ptr(w), M, K, E, N, _ptr(offsets),
                                               _ptr(dx), _ptr(dw), DTYPES[wt], _ptr(ws), ws.numel(), _stream(stream)),
            "nvfp4moe_grouped_mm_backward")
+    _keep(stream, dx, dw, ws)
     return dx, dw
 
 
@@ -918,6 +929,7 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None, a
         ws = _workspace(linear_workspace_bytes(M, K, N), x.device)
     _check(lib().nvfp4moe_linear(DTYPES[dt], _ptr(x), M, K, _ptr(w), N, _ptr(bias), a, _ptr(residual), _ptr(z),
                                  _ptr(out), _ptr(ws), ws.numel(), _stream(stream)), "nvfp4moe_linear")
+    _keep(stream, out, z, ws)
     return (out, z) if save_z else out
 
 
@@ -954,6 +966,7 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, z: torch
     _check(lib().nvfp4moe_linear_backward(DTYPES[dt], _ptr(dy), _ptr(x), _ptr(w), _ptr(z), M, K, N, a, _ptr(dx),
                                           _ptr(dw), DTYPES[wt], _ptr(db), _ptr(ws), ws.numel(), _stream(stream)),
            "nvfp4moe_linear_backward")
+    _keep(stream, dx, dw, db, ws)
     return dx, dw, db
 
 
@@ -975,6 +988,7 @@ def layer_norm(x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.T
     _check(lib().nvfp4moe_layer_norm(DTYPES[dt], _ptr(x), rows, cols, _ptr(gamma), _ptr(beta), float(eps),
                                      int(bool(rms)), _ptr(out), _ptr(mean), _ptr(rstd), _stream(stream)),
            "nvfp4moe_layer_norm")
+    _keep(stream, out, mean, rstd)
     return (out, mean, rstd) if stats else out
 
 
@@ -1010,4 +1024,5 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor |
                                               None if rms else _ptr(mean), _ptr(rstd), int(bool(rms)), _ptr(dx),
                                               _ptr(dgamma), _ptr(dbeta), _ptr(ws), ws.numel() if ws is not None else 0,
                                               _stream(stream)), "nvfp4moe_layer_norm_backward")
+    _keep(stream, dx, dgamma, dbeta, ws)
     return dx, dgamma, dbeta

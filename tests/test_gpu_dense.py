@@ -294,6 +294,78 @@ def test_gradients_against_differences():
         assert abs(lhs - rhs) <= tol, (lhs, rhs, tol)
 
 
+def test_outputs_and_workspaces_live_on_the_stream_given():
+    """What a call on another stream allocates is not handed out again while that stream still needs it,
+    even though the caller drops it at once and the current stream goes on allocating."""
+    x = torch.randn((4096, 2048), device="cuda").bfloat16()
+    w = torch.randn((2048, 2048), device="cuda").bfloat16()
+    g = torch.ones(2048, device="cuda")
+    side = torch.cuda.Stream()
+    want = moe.linear(x, w, act="silu", save_z=True)
+    grads = moe.linear_backward(x, x, w, z=want[1], act="silu", bias=True)
+    y, m, r = moe.layer_norm(x, g, g, stats=True)
+    ng = moe.layer_norm_backward(x, x, g, m, r)
+    torch.cuda.synchronize()
+    side.wait_stream(torch.cuda.current_stream())
+    kept = []
+    for _ in range(6):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(2_000_000)               # the side stream is behind the host
+        for i in range(3):
+            got = (moe.linear_backward(x, x, w, z=want[1], act="silu", bias=True, stream=side),
+                   moe.layer_norm_backward(x, x, g, m, r, stream=side))
+            if i == 2:
+                kept.append(got)
+            del got
+        junk = [torch.full((4096, 2048), float("nan"), device="cuda", dtype=torch.bfloat16) for _ in range(6)]
+        del junk
+    torch.cuda.synchronize()
+    for lin, nrm in kept:
+        assert all(torch.equal(a, b) for a, b in zip(lin, grads))
+        assert all(torch.equal(a, b) for a, b in zip(nrm, ng))
+
+
+def test_many_experts():
+    """The largest number of experts, most of them without rows."""
+    gen = torch.Generator().manual_seed(21)
+    E, K, N = 1024, 72, 40
+    counts = [0] * E
+    for e, c in ((0, 1), (1, 3), (31, 70), (32, 2), (500, 300), (1023, 65)):
+        counts[e] = c
+    off = offsets_of(counts)
+    x, dy = rand(gen, off[-1], K), rand(gen, off[-1], N)
+    w = rand(gen, E, N, K, scale=K ** -0.5)
+    ws = torch.full((moe.grouped_mm_workspace_bytes(E),), 255, dtype=torch.uint8, device="cuda")
+    args = (x.cuda(), w.cuda(), dev_offsets(off))
+    y = moe.grouped_mm(*args, ws=ws)
+    assert moe.status_read(ws) == moe.OK
+    dx, dw = moe.grouped_mm_backward(dy.cuda(), *args, ws=ws)
+    assert moe.status_read(ws) == moe.OK
+    X, W, D = f64(x), f64(w), f64(dy)
+    check(y, dense.grouped_mm(X, W, off), acc_bound(K, dense.grouped_mm(np.abs(X), np.abs(W), off)), "y")
+    DX, DW = dense.grouped_mm_backward(D, X, W, off)
+    SDX, SDW = dense.grouped_mm_backward(np.abs(D), np.abs(X), np.abs(W), off)
+    check(dx, DX, acc_bound(N, SDX), "dx")
+    check(dw, DW, acc_bound(300, SDW), "dw")
+
+
+def test_workspace_contents_do_not_matter():
+    """The same results from workspaces full of ones and of zeros."""
+    gen = torch.Generator().manual_seed(22)
+    off = offsets_of([40, 0, 90, 3])
+    x, w = rand(gen, off[-1], 128).cuda(), rand(gen, 4, 264, 128).cuda()
+    dy, o = rand(gen, off[-1], 264).cuda(), dev_offsets(off)
+    got = []
+    for fill in (0, 255):
+        ws = lambda n: torch.full((n,), fill, dtype=torch.uint8, device="cuda")  # noqa: E731
+        a, b = ws(moe.grouped_mm_workspace_bytes(4)), ws(moe.linear_backward_workspace_bytes(133, 128, 264))
+        got.append((moe.grouped_mm(x, w, o, ws=a), *moe.grouped_mm_backward(dy, x, w, o, ws=a),
+                    moe.linear(x, w[0], ws=ws(moe.linear_workspace_bytes(133, 128, 264))),
+                    *moe.linear_backward(dy, x, w[0], z=dy, act="relu", bias=True, ws=b)))
+        assert moe.status_read(a) == moe.OK and moe.status_read(b) == moe.OK
+    assert all(torch.equal(p, q) for p, q in zip(*got))
+
+
 def test_another_stream_and_graph_replay():
     gen = torch.Generator().manual_seed(11)
     off = offsets_of([40, 0, 90, 3])

@@ -108,6 +108,24 @@ def test_without_parameters_in_place_and_empty(rms):
     assert dx0.shape == (0, 640) and (dg0 == 0).all() and (rms or (db0 == 0).all())
 
 
+@pytest.mark.parametrize("cols", [640, 5111, 9000, 20001])
+@pytest.mark.parametrize("rows", [5, 400])
+def test_parameters_of_any_alignment(rows, cols):
+    """gamma and beta need 4-byte alignment only."""
+    x, dy = torch.randn(rows, cols).bfloat16().cuda(), torch.randn(rows, cols).bfloat16().cuda()
+    buf = torch.randn(2, cols + 3).cuda()
+    ref = None
+    for shift in (0, 1, 3):
+        g, b = torch.zeros(cols + shift).cuda()[shift:], torch.zeros(cols + shift).cuda()[shift:]
+        g.copy_(buf[0, :cols])
+        b.copy_(buf[1, :cols])
+        assert g.data_ptr() % 16 == 4 * shift
+        y, m, r = moe.layer_norm(x, g, b, stats=True)
+        got = (y, m, r, *moe.layer_norm_backward(dy, x, g, m, r))
+        ref = ref or got
+        assert all(torch.equal(p, q) for p, q in zip(ref, got))
+
+
 def test_large_offset_keeps_its_digits():
     """FP32 rows of 1000 + small noise: the variance is that of the noise (centred sums)."""
     gen = torch.Generator().manual_seed(3)
