@@ -449,8 +449,6 @@ MmArgs product_args(const ProductWs& p, bool ragged, int E, int64_t M, int32_t d
   m.fp16 = dtype == NVFP4MOE_FP16;
   m.status = &p.hdr->status;
   m.work_counter = ragged ? &p.hdr->work[0] : nullptr;
-  // a dense product needs nothing of the kernel that resets the status word
-  m.late_wait = !ragged;
   return m;
 }
 
@@ -1805,7 +1803,7 @@ int nvfp4moe_linear_backward(int32_t dtype, const void* dy, const void* x, const
   const void* dz = act != NVFP4MOE_ACT_NONE ? p.dz : dy;
   MmArgs m = product_args(p, false, 1, M, dtype);
   // with db the kernel before is the sum of its partials, which dz's has finished before
-  m.late_wait = act == NVFP4MOE_ACT_NONE || db != nullptr;
+  m.late_wait = db != nullptr;
   if (product_gradients(p, m, dz, x, w, K, N, dx, dw, dw_dtype, s) != cudaSuccess) return cuda_failed();
   return NVFP4MOE_OK;
 }

@@ -154,6 +154,12 @@ __device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
       : "memory");
 }
 
+// The same on this CTA's `bar` alone.
+__device__ __forceinline__ void tc_commit_pair_local(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+
 __device__ __forceinline__ void mma_f16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                              uint32_t accumulate) {
   asm volatile(
@@ -222,8 +228,11 @@ __device__ __forceinline__ Tile tile_at(const MmArgs& p, int w, int tile_i, int 
     local = w;
   }
   if (p.seg != nullptr) {
-    seg_row = p.seg[2 * t.e];
-    seg_rows = p.seg[2 * t.e + 1];
+    // wgrad may have started before its stream's previous kernel ended, so without the wait that makes
+    // earlier kernels' writes visible to plain loads: the table, which is complete by then, is read
+    // past the L1, which could hold an earlier call's
+    seg_row = kMode == kMmWgrad ? 0 : p.seg[2 * t.e];
+    seg_rows = kMode == kMmWgrad ? __ldcg(p.seg + 2 * t.e + 1) : p.seg[2 * t.e + 1];
   }
   const int block = local / (kRasterRows * ntj);
   const int in_block = local - block * kRasterRows * ntj;
@@ -256,14 +265,17 @@ __device__ __forceinline__ int pair_columns(int rows) { return (rows + 31) & ~31
 constexpr int kPieceBytes = 32 * 128;    // 32 rows of 128 bytes, 128-byte swizzle
 
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-// Until this thread's bulk stores have read shared memory / have been written.
-__device__ __forceinline__ void bulk_wait_read0() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+// Until all but this thread's last bulk store have read shared memory / all have been written.
+__device__ __forceinline__ void bulk_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_all0() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-// Stores 128 bytes of each of 32 rows (this lane's: w) at column c0, row c1 of matrix c2.
-__device__ __forceinline__ void store_piece(const void* tmap, uint8_t* piece, const uint32_t* w, int c0, int c1,
-                                            int c2, int lane) {
-  if (lane == 0) bulk_wait_read0();          // the piece before has been read
+// Stores 128 bytes of each of 32 rows (this lane's: w) at column c0, row c1 of matrix c2, through the
+// warp's two pieces of shared memory in turn.
+__device__ __forceinline__ void store_piece(const void* tmap, uint8_t* pieces, int& turn, const uint32_t* w, int c0,
+                                            int c1, int c2, int lane) {
+  uint8_t* piece = pieces + turn * kPieceBytes;
+  turn ^= 1;
+  if (lane == 0) bulk_wait_read1();          // the piece stored from here before has been read
   __syncwarp();
 #pragma unroll
   for (int i = 0; i < 8; ++i)
@@ -286,7 +298,8 @@ constexpr int kWorkRing = 4;             // tiles the loads may run ahead of the
 struct __align__(1024) PairSmem {
   uint8_t a[kPairStages][kOperandBytes];
   uint8_t b[kPairStages][kOperandBytes];
-  uint8_t epi[kPairEpiWarps * sizeof(EpilogueTile)];   // 1024-byte aligned: wgrad's pieces of 4 KB a warp
+  // forward, dgrad: an EpilogueTile a warp; wgrad: two pieces of 4 KB a warp (1024-byte aligned)
+  uint8_t epi[kPairEpiWarps * 2 * kPieceBytes];
   uint64_t full[kPairStages];        // (first CTA) both CTAs' loads of the stage have landed
   uint64_t empty[kPairStages];   // the MMAs have read the stage
   uint64_t acc_full[2];
@@ -367,7 +380,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     if (elect_one()) {
       uint32_t stage = 0, phase = 0;
       bool ok = true;
-      int next = pair, map_e = -1;
+      int next = pair, after = -1, map_e = -1;
       for (int it = 0; ok; ++it) {
         const int slot = it & (kWorkRing - 1);
         int w;
@@ -378,8 +391,13 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             break;
           }
           w = next < total ? next : -1;
-          // the one after it, under way while this one's loads are issued
-          if (w >= 0) next = p.work_counter != nullptr ? pairs + atomicAdd(p.work_counter, 1) : next + pairs;
+          // the ones after it are asked for two tiles ahead, so that the answers are there in time
+          if (p.work_counter == nullptr) {
+            next += pairs;
+          } else if (w >= 0) {
+            next = it == 0 ? pairs + atomicAdd(p.work_counter, 1) : after;
+            after = pairs + atomicAdd(p.work_counter, 1);
+          }
           store_rank(&s.work[slot], &s.work_full[slot], 1, w);
           s.work[slot] = w;
           mbar_arrive(&s.work_full[slot]);
@@ -435,8 +453,17 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
           if (++stage == kPairStages) { stage = 0; phase ^= 1u; }
         }
       }
-      // Every copy has landed once the pair's last MMAs have read it, which the cluster barrier at
-      // the end waits for.  A pair that gives up has none: its copies get a millisecond to land.
+      // The MMAs' completion arrives on both CTAs' `empty` barriers asynchronously, and nothing else of
+      // this CTA waits for the last of those arrivals: without this one could reach the shared memory
+      // of a CTA that has exited, or of the next kernel's.  It also shows that every copy has landed.
+      for (int i = 0; ok && i < kPairStages; ++i) {
+        if (!wait_cluster(&s.empty[stage], phase ^ 1u, &s.abort_flag)) {
+          set_abort(&s.abort_flag, p.status);
+          ok = false;
+        }
+        if (++stage == kPairStages) { stage = 0; phase ^= 1u; }
+      }
+      // A pair that gives up does not know what is under way: a millisecond for it to arrive.
       if (!ok) {
         const uint64_t t0 = globaltimer_ns();
         while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(10000);
@@ -488,7 +515,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         ++it;
       }
       // every tensor-core operation of the pair is done before the memories are given back
-      tc_commit_pair(&s.drain);
+      tc_commit_pair_local(&s.drain);
       if (!mbar_wait(&s.drain, 0)) set_abort(&s.abort_flag, p.status);
     }
   } else if (warp >= 4) {
@@ -496,7 +523,8 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     const int q = warp & 3;                  // tensor-memory lane quarter this warp may read
     const int part = (warp - 4) >> 2;        // which of the quarter's two warps
     EpilogueTile& tile = reinterpret_cast<EpilogueTile*>(s.epi)[warp - 4];
-    uint8_t* piece = s.epi + (warp - 4) * kPieceBytes;
+    uint8_t* pieces = s.epi + (warp - 4) * 2 * kPieceBytes;
+    int turn = 0;
     int it = 0;                              // tiles with an accumulator
     for (int n = 0;; ++n) {
       const int w = next_tile<true>(s, n, lane);
@@ -528,31 +556,44 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
           }
         }
       } else {
-        if (t.rows_valid > lane0) {            // rows and columns behind the output's are clipped by the map
-          for (int c = 64 * part; c < kPairTile && t.b0 + c < p.J; c += 128) {
-            uint32_t v[64];
-            if (has_acc) {
-              tmem_ld_32x32b_x32(acc + c, v);
-              tmem_ld_32x32b_x32(acc + c + 32, v + 32);
-              tmem_ld_wait();
-            } else {
+        // this warp's 64-column pieces, all in registers before any is stored, so that the accumulator is
+        // free early
+        uint32_t v[2][64];
 #pragma unroll
-              for (int i = 0; i < 64; ++i) v[i] = 0u;
-            }
-            if (p.out_f32) {
-              store_piece(&map_out, piece, v, t.b0 + c, t.a0 + lane0, t.e, lane);
-              if (t.b0 + c + 32 < p.J) store_piece(&map_out, piece, v + 32, t.b0 + c + 32, t.a0 + lane0, t.e, lane);
-            } else {
-              uint32_t h[32];
+        for (int j = 0; j < 2; ++j) {
+          if (has_acc) {
+            tmem_ld_32x32b_x32(acc + 64 * part + 128 * j, v[j]);
+            tmem_ld_32x32b_x32(acc + 64 * part + 128 * j + 32, v[j] + 32);
+          } else {
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                h[i] = pack16(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), p.fp16 != 0);
-              store_piece(&map_out, piece, h, t.b0 + c, t.a0 + lane0, t.e, lane);
-            }
+            for (int i = 0; i < 64; ++i) v[j][i] = 0u;
+          }
+        }
+        if (has_acc) {
+          tmem_ld_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_rank(&s.acc_empty[it & 1], 0);
+          ++it;
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int col = t.b0 + 64 * part + 128 * j, row = t.a0 + lane0;
+          // rows and columns behind the output's are clipped by the map
+          if (lane0 >= t.rows_valid || col >= p.J) continue;
+          if (p.out_f32) {
+            store_piece(&map_out, pieces, turn, v[j], col, row, t.e, lane);
+            if (col + 32 < p.J) store_piece(&map_out, pieces, turn, v[j] + 32, col + 32, row, t.e, lane);
+          } else {
+            uint32_t h[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              h[i] = pack16(__uint_as_float(v[j][2 * i]), __uint_as_float(v[j][2 * i + 1]), p.fp16 != 0);
+            store_piece(&map_out, pieces, turn, h, col, row, t.e, lane);
           }
         }
       }
-      if (has_acc) {
+      if (kTokens && has_acc) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_rank(&s.acc_empty[it & 1], 0);
@@ -567,6 +608,9 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
   cluster_sync();
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
+  // the pair gives its tensor memory back together: neither CTA exits before the other has
+  __syncwarp();
+  cluster_sync();
   if (p.late_wait) pdl_wait();
 }
 
@@ -714,8 +758,16 @@ mm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
           if (++stage == kStages) { stage = 0; phase ^= 1u; }
         }
       }
-      // every copy this thread started has landed before the CTA can exit
-      for (int i = 0; i < kStages; ++i)
+      // the MMAs have read every stage: no copy and no arrival of theirs is under way at the exit
+      for (int i = 0; ok && i < kStages; ++i) {
+        if (!wait_cluster(&s.empty[stage], phase ^ 1u, &s.abort_flag)) {
+          set_abort(&s.abort_flag, p.status);
+          ok = false;
+        }
+        if (++stage == kStages) { stage = 0; phase ^= 1u; }
+      }
+      // after giving up, the copies at least have landed
+      for (int i = 0; !ok && i < kStages; ++i)
         if ((issued >> i) & 1u)
           if (!mbar_wait(&s.full[i], (issued_par >> i) & 1u)) set_abort(&s.abort_flag, p.status);
     }
@@ -836,21 +888,10 @@ __global__ void __launch_bounds__(kMaxGroups) mm_table_kernel(const int32_t* off
   __shared__ int warp_sum[32];
   __shared__ __align__(128) uint32_t s_map[32][32];
   pdl_wait();
-  const int e = threadIdx.x, lane = e & 31, warp = e >> 5;
-  if (offsets == nullptr) {
-    // a dense product may run beside this kernel: it starts after these stores
-    if (e == 0) {
-      hdr->status = 0u;
-      hdr->work[0] = hdr->work[1] = 0;
-      __threadfence();
-    }
-    __syncwarp();
-    pdl_trigger();
-    return;
-  }
   pdl_trigger();
+  const int e = threadIdx.x, lane = e & 31, warp = e >> 5;
   int64_t lo = 0, hi = 0;
-  if (e < E) {
+  if (offsets != nullptr && e < E) {
     lo = offsets[e];
     hi = offsets[e + 1];
   }
@@ -859,6 +900,7 @@ __global__ void __launch_bounds__(kMaxGroups) mm_table_kernel(const int32_t* off
     hdr->status = bad ? kStatusBadInput : 0u;
     hdr->work[0] = hdr->work[1] = 0;
   }
+  if (offsets == nullptr) return;
   if (bad) lo = hi = 0;
   const int n = (int)((hi - lo + tile_rows - 1) / tile_rows);
   int sum = n;
@@ -881,8 +923,9 @@ __global__ void __launch_bounds__(kMaxGroups) mm_table_kernel(const int32_t* off
   __syncthreads();                        // the segments are written (read back below)
   for (int m = warp; m < 2 * E; m += blockDim.x >> 5) {
     const int which = m & 1;
-    const int first = t.seg[2 * (m >> 1)], count = t.seg[2 * (m >> 1) + 1];
-    if (count == 0) continue;             // never loaded from
+    // an empty segment's map is never loaded from; it is a valid one all the same
+    const int rows_of = t.seg[2 * (m >> 1) + 1], count = rows_of > 0 ? rows_of : 1;
+    const int first = rows_of > 0 ? t.seg[2 * (m >> 1)] : 0;
     __syncwarp();
     s_map[warp][lane] = reinterpret_cast<const uint32_t*>(which == 0 ? &maps.a : &maps.b)[lane];
     __syncwarp();
@@ -924,6 +967,7 @@ cudaError_t launch_pair(const void* a, const void* b, const MmArgs& args, int ti
   if (err != 0) return cudaErrorInvalidValue;
   const size_t smem = sizeof(PairSmem) + 1024;
   static_assert(sizeof(PairSmem) + 1024 <= 232448, "shared memory exceeds the per-block limit");
+  static_assert(kPairEpiWarps * sizeof(EpilogueTile) <= sizeof(PairSmem::epi), "the epilogue's tiles");
   const cudaError_t ce = allow_smem(reinterpret_cast<const void*>(mm_pair_kernel<kMode>), smem);
   if (ce != cudaSuccess) return ce;
   const int64_t ntj = (m.J + kPairTile - 1) / kPairTile;

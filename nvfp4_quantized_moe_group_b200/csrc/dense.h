@@ -59,9 +59,11 @@ struct MmArgs {
   const void* residual;  // [rows][J] or nullptr, the operands' type
   void* z_out;           // [rows][J] or nullptr: the sums with the bias, before the activation
   uint32_t* status;
-  int late_wait;         // the previous kernel of the stream is not one this product depends on, and has
+  int late_wait;         // The previous kernel of the stream is not one this product depends on, and has
                          // itself waited for those it does: it may run beside that kernel, and waits
-                         // for it only before it ends (so that the kernel after it can wait for both)
+                         // for it only before it ends (so that the kernel after it can wait for both).
+                         // For products whose inputs all come by TMA (no bias, no residual): plain
+                         // loads would see earlier kernels' writes only after the wait.
   int* work_counter;     // pairs; zero at launch: tiles handed out beyond the first of each CTA pair
                          // (nullptr: fixed turns, for tiles of one cost)
   int tile_rows;         // pairs: most token rows of a tile (set by launch_mm)
