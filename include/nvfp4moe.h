@@ -554,7 +554,7 @@ NVFP4MOE_API int nvfp4moe_forward_fp8(const nvfp4moe_fp8_experts* experts, const
  * 16-byte aligned unless stated otherwise, and outputs do not overlap inputs unless stated.
  *
  * Products take BF16 or FP16 operands, accumulate in FP32 on the tensor cores and round each
- * result once.  Limits: 0 <= M < 2^30, K and N multiples of 8 from 8 to 2^19, 1 <= E <= 1024,
+ * result once.  Limits: 0 <= M < 2^25, K and N multiples of 8 from 8 to 2^19, 1 <= E <= 1024,
  * M * K, M * N and E * K * N below 2^40; outside them NVFP4MOE_ERR_SHAPE. */
 enum { NVFP4MOE_BF16 = 0, NVFP4MOE_FP16 = 1, NVFP4MOE_FP32 = 2 };   /* element types */
 

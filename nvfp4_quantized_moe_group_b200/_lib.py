@@ -208,22 +208,26 @@ def _require(*specs):
     checked before devices.
     The library receives raw pointers, so a tensor of the wrong type or size would be read out
     of bounds rather than rejected."""
-    present = [s for s in specs if s[0] is not None]
-    for t, name, dtype, shape in present:
+    device = elsewhere = None
+    for t, name, dtype, shape in specs:
+        if t is None:
+            continue
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
-        if t.dtype != dtype:
+        if t.dtype is not dtype:
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
         if shape is not None and t.shape != shape:
             raise TypeError(f"{name} must have shape {tuple(int(s) for s in shape)}, got {tuple(t.shape)}")
         if not t.is_contiguous():
             raise TypeError(f"{name} must be contiguous")
-    if not present:
+        if device is None:
+            device = t.device
+        if elsewhere is None and (not t.is_cuda or t.device != device):
+            elsewhere = (t, name)
+    if device is None:
         return
-    device = present[0][0].device
-    for t, name, _, _ in present:
-        if not t.is_cuda or t.device != device:
-            raise TypeError(f"{name} must be a CUDA tensor on {device}, got {t.device}")
+    if elsewhere is not None:
+        raise TypeError(f"{elsewhere[1]} must be a CUDA tensor on {device}, got {elsewhere[0].device}")
     # the library launches on the current device: tensors of another one would be read
     # through addresses that device does not map
     if device.index != torch.cuda.current_device():
@@ -865,7 +869,7 @@ def grouped_mm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, out: tor
     _require((x, "x", dt, None), (w, "w", dt, (E, N, K)), (offsets, "offsets", torch.int32, (E + 1,)),
              (out, "out", dt, (M, N)), (ws, "ws", torch.uint8, None))
     if out is None:
-        out = torch.empty((M, N), dtype=dt, device=x.device)
+        out = x.new_empty((M, N))
     if ws is None:
         ws = _workspace(grouped_mm_workspace_bytes(E), x.device)
     _check(lib().nvfp4moe_grouped_mm(DTYPES[dt], _ptr(x), M, K, _ptr(w), E, N, _ptr(offsets), _ptr(out), _ptr(ws),
@@ -891,9 +895,9 @@ def grouped_mm_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, offs
              (offsets, "offsets", torch.int32, (E + 1,)), (dx, "dx", dt, (M, K)), (dw, "dw", wt, (E, N, K)),
              (ws, "ws", torch.uint8, None))
     if dx is None and need_dx:
-        dx = torch.empty((M, K), dtype=dt, device=dy.device)
+        dx = dy.new_empty((M, K))
     if dw is None and need_dw:
-        dw = torch.empty((E, N, K), dtype=wt, device=dy.device)
+        dw = dy.new_empty((E, N, K), dtype=wt)
     if ws is None:
         ws = _workspace(grouped_mm_workspace_bytes(E), dy.device)
     _check(lib().nvfp4moe_grouped_mm_backward(DTYPES[dt], _ptr(dy), _ptr(x), _ptr(w), M, K, E, N, _ptr(offsets),
@@ -923,8 +927,8 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None, a
     _require((x, "x", dt, None), (w, "w", dt, (N, K)), (bias, "bias", torch.float32, (N,)),
              (residual, "residual", dt, (M, N)), (out, "out", dt, (M, N)), (ws, "ws", torch.uint8, None))
     if out is None:
-        out = torch.empty((M, N), dtype=dt, device=x.device)
-    z = torch.empty((M, N), dtype=dt, device=x.device) if save_z else None
+        out = x.new_empty((M, N))
+    z = torch.empty_like(out) if save_z else None
     if ws is None:
         ws = _workspace(linear_workspace_bytes(M, K, N), x.device)
     _check(lib().nvfp4moe_linear(DTYPES[dt], _ptr(x), M, K, _ptr(w), N, _ptr(bias), a, _ptr(residual), _ptr(z),
@@ -957,10 +961,10 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, z: torch
              (dx, "dx", dt, (M, K)), (dw, "dw", wt, (N, K)), (ws, "ws", torch.uint8, None))
     dev = dy.device
     if dx is None and need_dx:
-        dx = torch.empty((M, K), dtype=dt, device=dev)
+        dx = dy.new_empty((M, K))
     if dw is None and need_dw:
-        dw = torch.empty((N, K), dtype=wt, device=dev)
-    db = torch.empty(N, dtype=torch.float32, device=dev) if bias else None
+        dw = dy.new_empty((N, K), dtype=wt)
+    db = dy.new_empty(N, dtype=torch.float32) if bias else None
     if ws is None:
         ws = _workspace(linear_backward_workspace_bytes(M, K, N), dev)
     _check(lib().nvfp4moe_linear_backward(DTYPES[dt], _ptr(dy), _ptr(x), _ptr(w), _ptr(z), M, K, N, a, _ptr(dx),
@@ -983,8 +987,8 @@ def layer_norm(x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.T
              (out, "out", dt, (rows, cols)))
     if out is None:
         out = torch.empty_like(x)
-    mean = torch.empty(rows, dtype=torch.float32, device=x.device) if stats and not rms else None
-    rstd = torch.empty(rows, dtype=torch.float32, device=x.device) if stats else None
+    mean = x.new_empty(rows, dtype=torch.float32) if stats and not rms else None
+    rstd = x.new_empty(rows, dtype=torch.float32) if stats else None
     _check(lib().nvfp4moe_layer_norm(DTYPES[dt], _ptr(x), rows, cols, _ptr(gamma), _ptr(beta), float(eps),
                                      int(bool(rms)), _ptr(out), _ptr(mean), _ptr(rstd), _stream(stream)),
            "nvfp4moe_layer_norm")
@@ -1016,8 +1020,8 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor |
         need_params = gamma is not None
     if dx is None:
         dx = torch.empty_like(dy)
-    dgamma = torch.empty(cols, dtype=torch.float32, device=dev) if need_params else None
-    dbeta = torch.empty(cols, dtype=torch.float32, device=dev) if need_params and not rms else None
+    dgamma = dy.new_empty(cols, dtype=torch.float32) if need_params else None
+    dbeta = torch.empty_like(dgamma) if need_params and not rms else None
     if ws is None and need_params:
         ws = _workspace(layer_norm_backward_workspace_bytes(rows, cols), dev)
     _check(lib().nvfp4moe_layer_norm_backward(DTYPES[dt], _ptr(dy), _ptr(x), rows, cols, _ptr(gamma),

@@ -389,8 +389,10 @@ constexpr int64_t kMaxElems = (int64_t)1 << 40;
 
 bool product_type(int32_t dtype) { return dtype == NVFP4MOE_BF16 || dtype == NVFP4MOE_FP16; }
 
+// M: a weight gradient's tile reduces over all rows, and its time (2^19 steps of 64 rows, under a
+// second) stays inside the limit of a wait.
 bool product_shape(int64_t M, int32_t K, int32_t N, int32_t E) {
-  if (M < 0 || M >= ((int64_t)1 << 30)) return false;
+  if (M < 0 || M >= ((int64_t)1 << 25)) return false;
   if (K < 8 || N < 8 || K % 8 != 0 || N % 8 != 0 || K > (1 << 19) || N > (1 << 19)) return false;
   if (E < 1 || E > kMaxGroups) return false;
   return M * (int64_t)(K > N ? K : N) < kMaxElems && (int64_t)K * N < kMaxElems / E;

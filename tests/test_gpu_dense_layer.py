@@ -171,6 +171,43 @@ def test_two_streams_at_once():
             assert all(torch.equal(p, q) for p, q in zip(a, b))
 
 
+def test_two_host_threads():
+    """Calls from two host threads, each on a stream of its own."""
+    import threading
+    w = torch.randn((6, 264, 512), device="cuda").bfloat16()
+    x = torch.randn((400, 512), device="cuda").bfloat16()
+    dy = torch.randn((400, 264), device="cuda").bfloat16()
+    o = torch.tensor([0, 3, 90, 90, 300, 301, 400], dtype=torch.int32, device="cuda")
+
+    def work():
+        y, (dx, dw) = moe.grouped_mm(x, w, o), moe.grouped_mm_backward(dy, x, w, o)
+        z, m, r = moe.layer_norm(x, stats=True)
+        return [y, dx, dw, z, moe.linear(x[:5], w[0]), *moe.linear_backward(dy, x, w[0], z=y, act="silu", bias=True),
+                *moe.layer_norm_backward(x, z, None, m, r, need_params=True)]
+
+    want = work()
+    torch.cuda.synchronize()
+    errors = []
+
+    def run():
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(40):
+                    got = work()
+                s.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(want, got))
+        except BaseException as e:      # noqa: BLE001  reported by the main thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=run) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+
+
 def test_offsets_beyond_32_bits():
     """Tensors of more than 2^31 elements (a row's offset passes 32 bits): sampled rows against FP64."""
     torch.cuda.empty_cache()

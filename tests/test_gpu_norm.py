@@ -108,6 +108,23 @@ def test_without_parameters_in_place_and_empty(rms):
     assert dx0.shape == (0, 640) and (dg0 == 0).all() and (rms or (db0 == 0).all())
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("cols", [3, 255, 1019, 5111, 9001, 20001])
+@pytest.mark.parametrize("rows", [7, 700])
+def test_in_place_rows_that_share_vectors(rows, cols, dtype):
+    """Rows of odd length share 16-byte vectors with their neighbours; in place, a neighbour may already
+    hold its result when a row is read."""
+    x, dy = torch.randn(rows, cols).to(dtype).cuda(), torch.randn(rows, cols).to(dtype).cuda()
+    g = torch.randn(cols).cuda()
+    y, m, r = moe.layer_norm(x, g, stats=True)
+    dx, dg, db = moe.layer_norm_backward(dy, x, g, m, r)
+    for _ in range(3):
+        x2, dy2 = x.clone(), dy.clone()
+        assert torch.equal(moe.layer_norm(x2, g, out=x2), y)
+        dx2, dg2, db2 = moe.layer_norm_backward(dy2, x, g, m, r, dx=dy2)
+        assert torch.equal(dx2, dx) and torch.equal(dg2, dg) and torch.equal(db2, db)
+
+
 @pytest.mark.parametrize("cols", [640, 5111, 9000, 20001])
 @pytest.mark.parametrize("rows", [5, 400])
 def test_parameters_of_any_alignment(rows, cols):
