@@ -72,7 +72,7 @@ def norm_backward(lib, **kw):
 
 
 SHAPES = [dict(K=0), dict(K=63), dict(K=12), dict(N=0), dict(N=4), dict(N=130), dict(K=(1 << 19) + 8),
-          dict(N=(1 << 19) + 8), dict(M=-1), dict(M=1 << 25), dict(M=(1 << 25) - 1, K=1 << 15)]
+          dict(N=(1 << 19) + 8), dict(M=-1), dict(M=1 << 25), dict(M=(1 << 25) - 1, K=(1 << 15) + 8)]
 
 
 @pytest.mark.parametrize("call", [grouped, grouped_backward, linear, linear_backward])
