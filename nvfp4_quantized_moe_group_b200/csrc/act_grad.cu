@@ -20,8 +20,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kCols = 256;               // columns of one CTA
 
+template <int kAct>
 __global__ void __launch_bounds__(kThreads)
-act_grad_kernel(const uint16_t* __restrict__ dy, const uint16_t* __restrict__ z, int64_t M, int N, int act, int fp16,
+act_grad_kernel(const uint16_t* __restrict__ dy, const uint16_t* __restrict__ z, int64_t M, int N, int fp16,
                 uint16_t* __restrict__ dz, float* __restrict__ partials, int64_t rows_per_block, WsHeader* hdr) {
   __shared__ float s_sum[8][kCols + 4];
   pdl_wait();
@@ -36,7 +37,7 @@ act_grad_kernel(const uint16_t* __restrict__ dy, const uint16_t* __restrict__ z,
   const int64_t r1 = r0 + rows_per_block < M ? r0 + rows_per_block : M;
   float sum[8] = {};
   if (col < N) {
-#pragma unroll 2
+#pragma unroll 4
     for (int64_t r = r0 + warp; r < r1; r += 8) {
       const int64_t at = r * N + col;
       const uint4 d4 = *reinterpret_cast<const uint4*>(dy + at);
@@ -48,14 +49,14 @@ act_grad_kernel(const uint16_t* __restrict__ dy, const uint16_t* __restrict__ z,
         v[2 * i] = f.x;
         v[2 * i + 1] = f.y;
       }
-      if (act != NVFP4MOE_ACT_NONE) {
+      if constexpr (kAct != NVFP4MOE_ACT_NONE) {
         const uint4 z4 = *reinterpret_cast<const uint4*>(z + at);
         const uint32_t zz[4] = {z4.x, z4.y, z4.z, z4.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float2 f = unpack16(zz[i], fp16 != 0);
-          v[2 * i] *= act_slope(f.x, act);
-          v[2 * i + 1] *= act_slope(f.y, act);
+          v[2 * i] *= act_slope<kAct>(f.x);
+          v[2 * i + 1] *= act_slope<kAct>(f.y);
         }
         *reinterpret_cast<uint4*>(dz + at) =
             make_uint4(pack16(v[0], v[1], fp16 != 0), pack16(v[2], v[3], fp16 != 0), pack16(v[4], v[5], fp16 != 0),
@@ -113,9 +114,12 @@ cudaError_t launch_act_grad(const void* dy, const void* z, int64_t M, int N, int
                             float* partials, WsHeader* hdr, int* launches, cudaStream_t stream) {
   const int n = act_grad_partials(M, N);
   const int64_t rows = (M + n - 1) / n;
-  cudaError_t e = launch_pdl(act_grad_kernel, dim3((N + kCols - 1) / kCols, n), dim3(kThreads), 0, stream,
-                             static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(z), M, N, act,
-                             fp16 ? 1 : 0, static_cast<uint16_t*>(dz), db != nullptr ? partials : nullptr, rows, hdr);
+  cudaError_t e = cudaSuccess;
+  with_act(act, [&](auto c) {
+    e = launch_pdl(act_grad_kernel<decltype(c)::value>, dim3((N + kCols - 1) / kCols, n), dim3(kThreads), 0, stream,
+                   static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(z), M, N, fp16 ? 1 : 0,
+                   static_cast<uint16_t*>(dz), db != nullptr ? partials : nullptr, rows, hdr);
+  });
   if (e != cudaSuccess) return e;
   ++*launches;
   if (db == nullptr) return cudaSuccess;

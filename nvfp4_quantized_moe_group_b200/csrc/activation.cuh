@@ -16,36 +16,54 @@ constexpr float kSqrt2OverPi = 0.79788456080286536f;
 // 1 / (1 + exp(-z)); exp(-z) = inf gives 0.
 __device__ __forceinline__ float sigmoid_f(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
 
-// NaN stays NaN in every activation.
-__device__ __forceinline__ float act_value(float z, int act) {
-  switch (act) {
-    case NVFP4MOE_ACT_RELU: return z < 0.0f ? 0.0f : z;
-    case NVFP4MOE_ACT_SILU: return z * sigmoid_f(z);
-    case NVFP4MOE_ACT_GELU: return 0.5f * z * (1.0f + erff(z * kSqrtHalf));
-    // 0.5 (1 + tanh(u)) = 1 / (1 + exp(-2u))
-    case NVFP4MOE_ACT_GELU_TANH: return z * sigmoid_f(2.0f * kSqrt2OverPi * (z + 0.044715f * z * z * z));
-    default: return z;
-  }
+// NaN stays NaN in every activation.  The activation is a template argument, chosen once per tile or
+// launch: chosen per value it became an indirect jump per value (8192 x 8192, K = 64, ReLU: 239 us
+// against 72 without an activation).
+template <int kAct>
+__device__ __forceinline__ float act_value(float z) {
+  if constexpr (kAct == NVFP4MOE_ACT_RELU) return z < 0.0f ? 0.0f : z;
+  else if constexpr (kAct == NVFP4MOE_ACT_SILU) return z * sigmoid_f(z);
+  else if constexpr (kAct == NVFP4MOE_ACT_GELU) return 0.5f * z * (1.0f + erff(z * kSqrtHalf));
+  // 0.5 (1 + tanh(u)) = 1 / (1 + exp(-2u))
+  else if constexpr (kAct == NVFP4MOE_ACT_GELU_TANH)
+    return z * sigmoid_f(2.0f * kSqrt2OverPi * (z + 0.044715f * z * z * z));
+  else return z;
 }
 
 // d act / dz
-__device__ __forceinline__ float act_slope(float z, int act) {
+template <int kAct>
+__device__ __forceinline__ float act_slope(float z) {
+  if constexpr (kAct == NVFP4MOE_ACT_RELU) {
+    return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
+  } else if constexpr (kAct == NVFP4MOE_ACT_SILU) {
+    const float p = sigmoid_f(z);
+    return p * (1.0f + z * (1.0f - p));
+  } else if constexpr (kAct == NVFP4MOE_ACT_GELU) {
+    return 0.5f * (1.0f + erff(z * kSqrtHalf)) + z * __expf(-0.5f * z * z) * kInvSqrt2Pi;
+  } else if constexpr (kAct == NVFP4MOE_ACT_GELU_TANH) {
+    const float z2 = z * z;
+    const float p = sigmoid_f(2.0f * kSqrt2OverPi * (z + 0.044715f * z * z2));
+    // p + z p (1 - p) d(2u)/dz; far out the second term's first factors are 0 and z2 may be inf
+    const float q = z * p * (1.0f - p);
+    return q == 0.0f ? p : p + q * (2.0f * kSqrt2OverPi) * (1.0f + 3.0f * 0.044715f * z2);
+  } else {
+    return 1.0f;
+  }
+}
+
+// Calls f with the activation as an integral constant.
+template <int kAct>
+struct ActConst {
+  static constexpr int value = kAct;
+};
+template <typename F>
+__host__ __device__ __forceinline__ void with_act(int act, F&& f) {
   switch (act) {
-    case NVFP4MOE_ACT_RELU: return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
-    case NVFP4MOE_ACT_SILU: {
-      const float p = sigmoid_f(z);
-      return p * (1.0f + z * (1.0f - p));
-    }
-    case NVFP4MOE_ACT_GELU:
-      return 0.5f * (1.0f + erff(z * kSqrtHalf)) + z * __expf(-0.5f * z * z) * kInvSqrt2Pi;
-    case NVFP4MOE_ACT_GELU_TANH: {
-      const float z2 = z * z;
-      const float p = sigmoid_f(2.0f * kSqrt2OverPi * (z + 0.044715f * z * z2));
-      // p + z p (1 - p) d(2u)/dz; far out the second term's first factors are 0 and z2 may be inf
-      const float q = z * p * (1.0f - p);
-      return q == 0.0f ? p : p + q * (2.0f * kSqrt2OverPi) * (1.0f + 3.0f * 0.044715f * z2);
-    }
-    default: return 1.0f;
+    case NVFP4MOE_ACT_RELU: f(ActConst<NVFP4MOE_ACT_RELU>{}); break;
+    case NVFP4MOE_ACT_SILU: f(ActConst<NVFP4MOE_ACT_SILU>{}); break;
+    case NVFP4MOE_ACT_GELU: f(ActConst<NVFP4MOE_ACT_GELU>{}); break;
+    case NVFP4MOE_ACT_GELU_TANH: f(ActConst<NVFP4MOE_ACT_GELU_TANH>{}); break;
+    default: f(ActConst<NVFP4MOE_ACT_NONE>{});
   }
 }
 

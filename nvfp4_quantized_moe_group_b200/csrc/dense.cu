@@ -20,7 +20,7 @@
 //
 // Per CTA: warp 0 loads (TMA, 128-byte swizzle), both CTAs' bytes counted on the first CTA's
 // barrier; warp 1 of the first CTA issues the MMAs; warps 4-11 run the epilogue: forward and dgrad
-// through padded shared-memory tiles, so that global accesses are whole 64-byte row pieces; wgrad,
+// transpose 32 x 32 pieces through shared memory, so that global accesses are whole 64-byte row pieces; wgrad,
 // whose rows are never ragged, by TMA stores of 128-byte x 32-row pieces (an expert's few rows make
 // few steps a tile, so wgrad is bound by its output: 64 experts of 128 rows, 5120 x 2560, 931 us
 // with the padded tiles and plain stores).
@@ -298,7 +298,7 @@ constexpr int kWorkRing = 4;             // tiles the loads may run ahead of the
 struct __align__(1024) PairSmem {
   uint8_t a[kPairStages][kOperandBytes];
   uint8_t b[kPairStages][kOperandBytes];
-  // forward, dgrad: an EpilogueTile a warp; wgrad: two pieces of 4 KB a warp (1024-byte aligned)
+  // wgrad: two pieces of 4 KB a warp (1024-byte aligned); forward, dgrad: three token pieces
   uint8_t epi[kPairEpiWarps * 2 * kPieceBytes];
   uint64_t full[kPairStages];        // (first CTA) both CTAs' loads of the stage have landed
   uint64_t empty[kPairStages];   // the MMAs have read the stage
@@ -522,7 +522,6 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     // ----------------------------------------------------------- epilogue ----
     const int q = warp & 3;                  // tensor-memory lane quarter this warp may read
     const int part = (warp - 4) >> 2;        // which of the quarter's two warps
-    EpilogueTile& tile = reinterpret_cast<EpilogueTile*>(s.epi)[warp - 4];
     uint8_t* pieces = s.epi + (warp - 4) * 2 * kPieceBytes;
     int turn = 0;
     int it = 0;                              // tiles with an accumulator
@@ -547,13 +546,45 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
       // the warps of a quarter take its 32-column pieces in turn
       if constexpr (kTokens) {
         if (t.b0 + lane0 < p.J) {
-          for (int c = 32 * part; c < t.rows_valid; c += 64) {
-            uint32_t v[32];
-            tmem_ld_32x32b_x32(acc + c, v);
-            tmem_ld_wait();
-            put_columns32(tile, v, lane);
-            store_tile32(tile, p, t.out_row + c, t.rows_valid - c, t.b0 + lane0, lane);
+          const int f0 = t.b0 + lane0;
+          const bool col_ok = f0 + (lane & 3) * 8 < p.J;      // J is a multiple of 8
+          float bias[4];
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const int f = f0 + 8 * b + (lane >> 2);
+            bias[b] = p.bias != nullptr && f < p.J ? __ldg(p.bias + f) : 0.0f;
           }
+          // the next piece's accumulator values and residual are on their way while one is stored
+          uint32_t v[2][2][16];
+          uint4 res[2][4];
+          auto fetch = [&](int c, int to) {
+            tmem_ld_16x256b_x4(acc + c, v[to][0]);
+            tmem_ld_16x256b_x4(acc + (16u << 16) + c, v[to][1]);
+            if (p.residual != nullptr) {
+              const uint16_t* from = static_cast<const uint16_t*>(p.residual) + f0 + (lane & 3) * 8;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int r = c + i * 8 + (lane >> 2);
+                res[to][i] = col_ok && r < t.rows_valid
+                                 ? *reinterpret_cast<const uint4*>(from + (t.out_row + r) * (int64_t)p.J)
+                                 : make_uint4(0, 0, 0, 0);
+              }
+            }
+          };
+          if (32 * part < t.rows_valid) fetch(32 * part, 0);
+          with_act(p.act, [&](auto act) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int c = 32 * part + 64 * j;
+              if (c < t.rows_valid) {
+                tmem_ld_wait();
+                if (c + 64 < t.rows_valid) fetch(c + 64, (j + 1) & 1);
+                store_piece32<decltype(act)::value>(p, pieces, v[j & 1], bias, res[j & 1],
+                                                    (t.out_row + c) * (int64_t)p.J + f0 + (lane & 3) * 8,
+                                                    t.rows_valid - c, col_ok, lane);
+              }
+            }
+          });
         }
       } else {
         // this warp's 64-column pieces, all in registers before any is stored, so that the accumulator is
@@ -848,20 +879,40 @@ mm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
       }
       const int col = t.b0 + 4 * lane;
       if (col < p.J) {                     // J is a multiple of 8
-        for (int r = rank + split * q; r < t.rows_valid; r += 4 * split) {
-          float4 v;
-          if (split == 1) {
-            v = *reinterpret_cast<const float4*>(&s.part[r][4 * lane]);
-          } else {
-            v = make_float4(0.f, 0.f, 0.f, 0.f);
-            const uint32_t at = smem_u32(&s.part[r][4 * lane]);
-            for (int c = 0; c < split; ++c) {
-              const float4 o = ld_cluster_f4(map_rank(at, c));
-              v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+        const float4 bias = p.bias != nullptr ? __ldg(reinterpret_cast<const float4*>(p.bias + col))
+                                              : make_float4(0.f, 0.f, 0.f, 0.f);
+        const int64_t at0 = t.out_row * (int64_t)p.J + col;
+        with_act(p.act, [&](auto act) {
+          // four rows at a time: their residual loads and the reads of the parts overlap
+          for (int r0 = rank + split * q; r0 < t.rows_valid; r0 += 16 * split) {
+            uint2 res[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = r0 + 4 * split * i;
+              res[i] = p.residual != nullptr && r < t.rows_valid
+                           ? *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.residual) + at0 +
+                                                             r * (int64_t)p.J)
+                           : make_uint2(0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = r0 + 4 * split * i;
+              if (r >= t.rows_valid) continue;
+              float4 v;
+              if (split == 1) {
+                v = *reinterpret_cast<const float4*>(&s.part[r][4 * lane]);
+              } else {
+                v = make_float4(0.f, 0.f, 0.f, 0.f);
+                const uint32_t at = smem_u32(&s.part[r][4 * lane]);
+                for (int c = 0; c < split; ++c) {
+                  const float4 o = ld_cluster_f4(map_rank(at, c));
+                  v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+                }
+              }
+              store4<decltype(act)::value>(p, v, bias, res[i], at0 + r * (int64_t)p.J);
             }
           }
-          store4(p, v, (t.out_row + r) * (int64_t)p.J + col, col);
-        }
+        });
       }
       __syncwarp();
       if (split == 1) {
@@ -967,7 +1018,7 @@ cudaError_t launch_pair(const void* a, const void* b, const MmArgs& args, int ti
   if (err != 0) return cudaErrorInvalidValue;
   const size_t smem = sizeof(PairSmem) + 1024;
   static_assert(sizeof(PairSmem) + 1024 <= 232448, "shared memory exceeds the per-block limit");
-  static_assert(kPairEpiWarps * sizeof(EpilogueTile) <= sizeof(PairSmem::epi), "the epilogue's tiles");
+  static_assert(3 * kTokenPiece <= 2 * kPieceBytes, "the epilogue's pieces");
   const cudaError_t ce = allow_smem(reinterpret_cast<const void*>(mm_pair_kernel<kMode>), smem);
   if (ce != cudaSuccess) return ce;
   const int64_t ntj = (m.J + kPairTile - 1) / kPairTile;
