@@ -20,8 +20,8 @@
 //
 // Per CTA: warp 0 loads (TMA, 128-byte swizzle), both CTAs' bytes counted on the first CTA's
 // barrier; warp 1 of the first CTA issues the MMAs; warps 4-11 run the epilogue: forward and dgrad
-// transpose 32 x 32 pieces through shared memory, so that global accesses are whole 64-byte row pieces; wgrad,
-// whose rows are never ragged, by TMA stores of 128-byte x 32-row pieces (an expert's few rows make
+// transpose 32 x 32 pieces through shared memory, stored by TMA from there (a segment's last rows, which no
+// map can clip, row by row); wgrad, whose rows are never ragged, in 128-byte x 32-row pieces (an expert's few rows make
 // few steps a tile, so wgrad is bound by its output: 64 experts of 128 rows, 5120 x 2560, 931 us
 // with the padded tiles and plain stores).
 //
@@ -264,11 +264,6 @@ __device__ __forceinline__ int pair_columns(int rows) { return (rows + 31) & ~31
 
 constexpr int kPieceBytes = 32 * 128;    // 32 rows of 128 bytes, 128-byte swizzle
 
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-// Until all but this thread's last bulk store have read shared memory / all have been written.
-__device__ __forceinline__ void bulk_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_all0() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-
 // Stores 128 bytes of each of 32 rows (this lane's: w) at column c0, row c1 of matrix c2, through the
 // warp's two pieces of shared memory in turn.
 __device__ __forceinline__ void store_piece(const void* tmap, uint8_t* pieces, int& turn, const uint32_t* w, int c0,
@@ -284,9 +279,7 @@ __device__ __forceinline__ void store_piece(const void* tmap, uint8_t* pieces, i
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncwarp();
   if (lane == 0) {
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(tmap),
-                 "r"(smem_u32(piece)), "r"(c0), "r"(c1), "r"(c2)
-                 : "memory");
+    tma_store_3d(tmap, piece, c0, c1, c2);
     bulk_commit();
   }
 }
@@ -298,7 +291,7 @@ constexpr int kWorkRing = 4;             // tiles the loads may run ahead of the
 struct __align__(1024) PairSmem {
   uint8_t a[kPairStages][kOperandBytes];
   uint8_t b[kPairStages][kOperandBytes];
-  // wgrad: two pieces of 4 KB a warp (1024-byte aligned); forward, dgrad: three token pieces
+  // wgrad: two pieces of 4 KB a warp (1024-byte aligned); forward, dgrad: four token pieces
   uint8_t epi[kPairEpiWarps * 2 * kPieceBytes];
   uint64_t full[kPairStages];        // (first CTA) both CTAs' loads of the stage have landed
   uint64_t empty[kPairStages];   // the MMAs have read the stage
@@ -330,7 +323,8 @@ template <int kMode>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                const __grid_constant__ CUtensorMap map_b64, const __grid_constant__ CUtensorMap map_b32,
-               const __grid_constant__ CUtensorMap map_out, const __grid_constant__ MmArgs p) {
+               const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_z,
+               const __grid_constant__ MmArgs p) {
   // forward, dgrad: A = the weights (i: output features), B = the token rows (j)
   constexpr bool kTokens = kMode != kMmWgrad;
   constexpr bool kAMn = kMode != kMmForward;
@@ -579,9 +573,8 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
               if (c < t.rows_valid) {
                 tmem_ld_wait();
                 if (c + 64 < t.rows_valid) fetch(c + 64, (j + 1) & 1);
-                store_piece32<decltype(act)::value>(p, pieces, v[j & 1], bias, res[j & 1],
-                                                    (t.out_row + c) * (int64_t)p.J + f0 + (lane & 3) * 8,
-                                                    t.rows_valid - c, col_ok, lane);
+                const PieceAt to{&map_out, &map_z, t.out_row + c, f0, t.rows_valid - c};
+                store_piece32<decltype(act)::value>(p, to, pieces, turn, v[j & 1], bias, res[j & 1], lane);
               }
             }
           });
@@ -631,7 +624,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         ++it;
       }
     }
-    if (kMode == kMmWgrad && lane == 0) bulk_wait_all0();
+    if (lane == 0) bulk_wait_all0();
   }
 
   __syncwarp();
@@ -1002,23 +995,25 @@ template <int kMode>
 cudaError_t launch_pair(const void* a, const void* b, const MmArgs& args, int tile_rows, cudaStream_t stream) {
   MmArgs m = args;
   m.tile_rows = tile_rows;
-  CUtensorMap map_a, map_b, map_b64, map_b32, map_out;
+  CUtensorMap map_a, map_b, map_b64, map_b32, map_out, map_z;
   int err;
   if (kMode == kMmWgrad) {
     err = make_tma_16(&map_a, a, m.I, m.rows, 1, kBK) | make_tma_16(&map_b, b, m.J, m.rows, 1, kBK) |
-          make_tma_3d(&map_out, m.out, m.out_f32 ? 4 : 2, m.J, m.I, m.E, 32);
-    map_b64 = map_b32 = map_b;
+          make_tma_3d(&map_out, m.out, m.out_f32 ? 4 : 2, m.J, m.I, m.E, 32, 128);
+    map_b64 = map_b32 = map_z = map_b;                 // not used
   } else {
     err = kMode == kMmForward ? make_tma_16(&map_a, b, m.R, m.J, m.E, kHalf)
                               : make_tma_16(&map_a, b, m.J, m.R, m.E, kBK);
     err |= make_tma_16(&map_b, a, m.R, m.rows, 1, kHalf) | make_tma_16(&map_b64, a, m.R, m.rows, 1, 64) |
            make_tma_16(&map_b32, a, m.R, m.rows, 1, 32);
-    map_out = map_b;       // not used: ragged rows cannot be clipped by a map
+    err |= make_tma_3d(&map_out, m.out, 2, m.J, m.rows, 1, 32, 64);
+    map_z = map_out;
+    if (m.z_out != nullptr) err |= make_tma_3d(&map_z, m.z_out, 2, m.J, m.rows, 1, 32, 64);
   }
   if (err != 0) return cudaErrorInvalidValue;
   const size_t smem = sizeof(PairSmem) + 1024;
   static_assert(sizeof(PairSmem) + 1024 <= 232448, "shared memory exceeds the per-block limit");
-  static_assert(3 * kTokenPiece <= 2 * kPieceBytes, "the epilogue's pieces");
+  static_assert(4 * kTokenPiece <= 2 * kPieceBytes, "the epilogue's pieces");
   const cudaError_t ce = allow_smem(reinterpret_cast<const void*>(mm_pair_kernel<kMode>), smem);
   if (ce != cudaSuccess) return ce;
   const int64_t ntj = (m.J + kPairTile - 1) / kPairTile;
@@ -1027,7 +1022,7 @@ cudaError_t launch_pair(const void* a, const void* b, const MmArgs& args, int ti
   most *= ntj;
   const int64_t pairs = num_sms() / 2;
   return launch_pdl(mm_pair_kernel<kMode>, dim3((unsigned)(2 * (most < pairs ? most : pairs))), dim3(kPairThreads),
-                    smem, stream, map_a, map_b, map_b64, map_b32, map_out, m);
+                    smem, stream, map_a, map_b, map_b64, map_b32, map_out, map_z, m);
 }
 
 template <int kMode, int kTok>

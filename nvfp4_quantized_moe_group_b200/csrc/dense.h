@@ -95,13 +95,13 @@ int act_grad_partials(int64_t M, int64_t N);
 cudaError_t launch_act_grad(const void* dy, const void* z, int64_t M, int N, int act, bool fp16, void* dz, float* db,
                             float* partials, WsHeader* hdr, int32_t* launches, cudaStream_t stream);
 
-// gemm.cu: tensor map of 2- or 4-byte elements [batch][rows][inner], a box of 128 bytes x box_rows x 1, 128B
-// swizzle.
+// gemm.cu: tensor map of 2- or 4-byte elements [batch][rows][inner], a box of box_bytes (64 or 128, the
+// swizzle's width too) x box_rows x 1.
 int make_tma_3d(CUtensorMap* map, const void* base, uint32_t elem_bytes, uint64_t inner, uint64_t rows,
-                uint64_t batch, uint32_t box_rows);
+                uint64_t batch, uint32_t box_rows, uint32_t box_bytes);
 inline int make_tma_16(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint64_t batch,
                        uint32_t box_rows) {
-  return make_tma_3d(map, base, 2, inner, rows, batch, box_rows);
+  return make_tma_3d(map, base, 2, inner, rows, batch, box_rows, 128);
 }
 
 }  // namespace nvfp4moe

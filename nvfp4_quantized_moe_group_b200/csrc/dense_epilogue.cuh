@@ -30,10 +30,24 @@ __device__ __forceinline__ void store4(const MmArgs& p, float4 f, float4 bias, u
 // The accumulator holds features along tensor-memory lanes and tokens along columns.  tcgen05.ld
 // 16x256b hands it out as 8 x 8 fragments (this thread: feature lane / 4, tokens 2 (lane % 4) and the
 // next), which stmatrix.trans stores as token rows of 8 features: 4 shared-memory instructions for the whole
-// piece (32 when each thread stores its values one by one).  A token row is 64 bytes, 80 apart: the 8
-// rows of a fragment, and 8 lanes' 16-byte reads, fall in different banks.
-constexpr int kPieceRow = 80;
-constexpr int kTokenPiece = 32 * kPieceRow;
+// piece (32 when each thread stores its values one by one).  A token row is 64 bytes in the 64-byte
+// swizzle of a TMA store, which takes the piece from there; the swizzle also puts a fragment's 8 rows
+// in different banks.  (Against plain 16-byte stores: 8192 x 5120, K = 5120, 592 -> 586 us.)
+constexpr int kTokenPiece = 32 * 64;
+
+// Byte of 16-byte chunk c of token row r.
+__device__ __forceinline__ uint32_t token_chunk(int r, int c) { return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4)); }
+
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// Until all but this thread's last bulk store have read shared memory / all have been written.
+__device__ __forceinline__ void bulk_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all0() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+__device__ __forceinline__ void tma_store_3d(const void* tmap, const void* src, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(tmap),
+               "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
 
 // 16 lanes x 32 columns: for k = 0..3, lane (i / 4) columns 8k + 2 (i % 4) + {0, 1} in r[4k], r[4k + 1] and
 // lane (i / 4 + 8) at the same columns in r[4k + 2], r[4k + 3].
@@ -49,46 +63,52 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t* r) 
 // Features 8 b .. 8 b + 7 of 32 tokens between this warp's piece and fragments (w[k]: tokens 8k .. 8k + 7).
 __device__ __forceinline__ void put_fragments(uint32_t piece, int b, const uint32_t* w, int lane) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
-                   piece + lane * kPieceRow + b * 16),
+                   piece + token_chunk(lane, b)),
                "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
                : "memory");
 }
 __device__ __forceinline__ void get_fragments(uint32_t piece, int b, uint32_t* w, int lane) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-               : "r"(piece + lane * kPieceRow + b * 16)
+               : "r"(piece + token_chunk(lane, b))
                : "memory");
 }
 
-// A piece's token rows (`live` of them, 64 bytes each) between shared memory and rows of the tensor: this
-// lane's 16 bytes of rows lane / 4, + 8, + 16, + 24.
+// The first `live` token rows of a piece to rows of the tensor, 16 bytes a lane.
 __device__ __forceinline__ void rows_to_global(uint16_t* base, const uint8_t* piece, int64_t at, int64_t J, int live,
                                                int lane) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = i * 8 + (lane >> 2);
     if (r < live)
-      *reinterpret_cast<uint4*>(base + at + r * J) =
-          *reinterpret_cast<const uint4*>(piece + r * kPieceRow + (lane & 3) * 16);
+      *reinterpret_cast<uint4*>(base + at + r * J) = *reinterpret_cast<const uint4*>(piece + token_chunk(r, lane & 3));
   }
 }
 
+// Where a piece goes: token row `row` on, feature f0 on (of J); `live` of its rows belong to the tile.
+struct PieceAt {
+  const void *map_y, *map_z;
+  int64_t row;
+  int f0;
+  int live;
+};
+
 // v: the accumulator's 32 x 32 values as two tmem_ld_16x256b_x4 give them; bias[b]: of feature 8 b + lane / 4;
-// res: this lane's residual vectors (rows as in rows_to_global).  at: first token row, column of this lane's
-// 8 features; col_ok: that column lies in the output.
+// res: this lane's residual vectors (rows lane / 4, + 8, + 16, + 24, features 8 (lane % 4) on).  pieces: the
+// warp's [2][y, z] pieces, used in turn.
 template <int kAct>
-__device__ __forceinline__ void store_piece32(const MmArgs& p, uint8_t* pieces, const uint32_t (*v)[16],
-                                              const float* bias, const uint4* res, int64_t at, int live, bool col_ok,
-                                              int lane) {
+__device__ __forceinline__ void store_piece32(const MmArgs& p, const PieceAt& to, uint8_t* pieces, int& turn,
+                                              const uint32_t (*v)[16], const float* bias, const uint4* res, int lane) {
   const bool fp16 = p.fp16 != 0;
-  uint8_t* p_y = pieces;
-  uint8_t* p_z = pieces + kTokenPiece;
-  uint8_t* p_r = pieces + 2 * kTokenPiece;
-  __syncwarp();                                  // the pieces before have been read
-  if (p.residual != nullptr) {
+  uint8_t* p_y = pieces + turn * 2 * kTokenPiece;
+  uint8_t* p_z = p_y + kTokenPiece;
+  turn ^= 1;
+  if (lane == 0) bulk_wait_read1();              // what was stored from here before has been read
+  __syncwarp();
+  if (p.residual != nullptr) {                   // through y's piece: a fragment is read before its place is written
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<uint4*>(p_r + (i * 8 + (lane >> 2)) * kPieceRow + (lane & 3) * 16) = res[i];
+      *reinterpret_cast<uint4*>(p_y + token_chunk(i * 8 + (lane >> 2), lane & 3)) = res[i];
     __syncwarp();
   }
 #pragma unroll
@@ -108,7 +128,7 @@ __device__ __forceinline__ void store_piece32(const MmArgs& p, uint8_t* pieces, 
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = act_value<kAct>(f[i]);
     if (p.residual != nullptr) {
-      get_fragments(smem_u32(p_r), b, w, lane);
+      get_fragments(smem_u32(p_y), b, w, lane);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float2 r = unpack16(w[k], fp16);
@@ -120,10 +140,21 @@ __device__ __forceinline__ void store_piece32(const MmArgs& p, uint8_t* pieces, 
     for (int k = 0; k < 4; ++k) w[k] = pack16(f[2 * k], f[2 * k + 1], fp16);
     put_fragments(smem_u32(p_y), b, w, lane);
   }
-  __syncwarp();
-  if (col_ok) {
-    if (p.z_out != nullptr) rows_to_global(static_cast<uint16_t*>(p.z_out), p_z, at, p.J, live, lane);
-    rows_to_global(static_cast<uint16_t*>(p.out), p_y, at, p.J, live, lane);
+  if (to.live >= 32) {                           // whole pieces: the map clips features behind J
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) {
+      if (p.z_out != nullptr) tma_store_3d(to.map_z, p_z, to.f0, (int)to.row, 0);
+      tma_store_3d(to.map_y, p_y, to.f0, (int)to.row, 0);
+      bulk_commit();
+    }
+  } else {                                       // a segment's last rows: the rows behind are not this tile's
+    __syncwarp();
+    if (to.f0 + (lane & 3) * 8 < p.J) {          // J is a multiple of 8
+      const int64_t at = to.row * p.J + to.f0 + (lane & 3) * 8;
+      if (p.z_out != nullptr) rows_to_global(static_cast<uint16_t*>(p.z_out), p_z, at, p.J, to.live, lane);
+      rows_to_global(static_cast<uint16_t*>(p.out), p_y, at, p.J, to.live, lane);
+    }
   }
 }
 

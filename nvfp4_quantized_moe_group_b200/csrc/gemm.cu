@@ -887,17 +887,17 @@ int make_tma_2d(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_t
 }
 
 int make_tma_3d(CUtensorMap* map, const void* base, uint32_t elem_bytes, uint64_t inner, uint64_t rows,
-                uint64_t batch, uint32_t box_rows) {
+                uint64_t batch, uint32_t box_rows, uint32_t box_bytes) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return -1;
   const cuuint64_t dims[3] = {inner, rows, batch};
   const cuuint64_t strides[2] = {inner * elem_bytes, inner * rows * elem_bytes};
-  const cuuint32_t box[3] = {128 / elem_bytes, box_rows, 1};
+  const cuuint32_t box[3] = {box_bytes / elem_bytes, box_rows, 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   const CUresult r = fn(map, elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT32, 3,
                         const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                        box_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? 0 : (int)r;
 }
 
