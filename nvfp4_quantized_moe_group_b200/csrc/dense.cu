@@ -548,34 +548,33 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             const int f = f0 + 8 * b + (lane >> 2);
             bias[b] = p.bias != nullptr && f < p.J ? __ldg(p.bias + f) : 0.0f;
           }
-          // the next piece's accumulator values and residual are on their way while one is stored
-          uint32_t v[2][2][16];
-          uint4 res[2][4];
-          auto fetch = [&](int c, int to) {
-            tmem_ld_16x256b_x4(acc + c, v[to][0]);
-            tmem_ld_16x256b_x4(acc + (16u << 16) + c, v[to][1]);
+          // the next piece's accumulator values and residual are on their way while one is stored; one
+          // copy of the code for all pieces, since straight-line code for all four ran at the rate of the
+          // instruction fetches
+          uint32_t v[2][16];
+          uint4 res[4];
+          auto fetch = [&](int c) {
+            if (c >= kPairTile || c >= t.rows_valid) return;
+            tmem_ld_16x256b_x4(acc + c, v[0]);
+            tmem_ld_16x256b_x4(acc + (16u << 16) + c, v[1]);
             if (p.residual != nullptr) {
               const uint16_t* from = static_cast<const uint16_t*>(p.residual) + f0 + (lane & 3) * 8;
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const int r = c + i * 8 + (lane >> 2);
-                res[to][i] = col_ok && r < t.rows_valid
-                                 ? *reinterpret_cast<const uint4*>(from + (t.out_row + r) * (int64_t)p.J)
-                                 : make_uint4(0, 0, 0, 0);
+                res[i] = col_ok && r < t.rows_valid
+                             ? *reinterpret_cast<const uint4*>(from + (t.out_row + r) * (int64_t)p.J)
+                             : make_uint4(0, 0, 0, 0);
               }
             }
           };
-          if (32 * part < t.rows_valid) fetch(32 * part, 0);
+          fetch(32 * part);
           with_act(p.act, [&](auto act) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int c = 32 * part + 64 * j;
-              if (c < t.rows_valid) {
-                tmem_ld_wait();
-                if (c + 64 < t.rows_valid) fetch(c + 64, (j + 1) & 1);
-                const PieceAt to{&map_out, &map_z, t.out_row + c, f0, t.rows_valid - c};
-                store_piece32<decltype(act)::value>(p, to, pieces, turn, v[j & 1], bias, res[j & 1], lane);
-              }
+#pragma unroll 1
+            for (int c = 32 * part; c < t.rows_valid; c += 64) {
+              tmem_ld_wait();
+              const PieceAt to{&map_out, &map_z, t.out_row + c, f0, t.rows_valid - c};
+              store_piece32<decltype(act)::value>(p, to, pieces, turn, v, bias, res, lane, [&] { fetch(c + 64); });
             }
           });
         }

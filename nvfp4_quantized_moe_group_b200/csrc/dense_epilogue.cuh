@@ -32,7 +32,7 @@ __device__ __forceinline__ void store4(const MmArgs& p, float4 f, float4 bias, u
 // next), which stmatrix.trans stores as token rows of 8 features: 4 shared-memory instructions for the whole
 // piece (32 when each thread stores its values one by one).  A token row is 64 bytes in the 64-byte
 // swizzle of a TMA store, which takes the piece from there; the swizzle also puts a fragment's 8 rows
-// in different banks.  (Against plain 16-byte stores: 8192 x 5120, K = 5120, 592 -> 586 us.)
+// in different banks.  (Against plain 16-byte stores: 4096 x 20480, K = 5120, 592 -> 586 us.)
 constexpr int kTokenPiece = 32 * 64;
 
 // Byte of 16-byte chunk c of token row r.
@@ -95,10 +95,11 @@ struct PieceAt {
 
 // v: the accumulator's 32 x 32 values as two tmem_ld_16x256b_x4 give them; bias[b]: of feature 8 b + lane / 4;
 // res: this lane's residual vectors (rows lane / 4, + 8, + 16, + 24, features 8 (lane % 4) on).  pieces: the
-// warp's [2][y, z] pieces, used in turn.
-template <int kAct>
+// warp's [2][y, z] pieces, used in turn.  next(): called once v and res have been used.
+template <int kAct, typename Next>
 __device__ __forceinline__ void store_piece32(const MmArgs& p, const PieceAt& to, uint8_t* pieces, int& turn,
-                                              const uint32_t (*v)[16], const float* bias, const uint4* res, int lane) {
+                                              const uint32_t (*v)[16], const float* bias, const uint4* res, int lane,
+                                              Next next) {
   const bool fp16 = p.fp16 != 0;
   uint8_t* p_y = pieces + turn * 2 * kTokenPiece;
   uint8_t* p_z = p_y + kTokenPiece;
@@ -140,6 +141,7 @@ __device__ __forceinline__ void store_piece32(const MmArgs& p, const PieceAt& to
     for (int k = 0; k < 4; ++k) w[k] = pack16(f[2 * k], f[2 * k + 1], fp16);
     put_fragments(smem_u32(p_y), b, w, lane);
   }
+  next();
   if (to.live >= 32) {                           // whole pieces: the map clips features behind J
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
