@@ -67,6 +67,18 @@ __host__ __device__ __forceinline__ void with_act(int act, F&& f) {
   }
 }
 
+// The same with the operands' type: f(ActConst<...>{}, BoolConst<fp16>{}).  Tested per value, the type costs a
+// branch per conversion.
+template <bool kValue>
+struct BoolConst {
+  static constexpr bool value = kValue;
+};
+template <typename F>
+__host__ __device__ __forceinline__ void with_act(int act, bool fp16, F&& f) {
+  if (fp16) with_act(act, [&](auto a) { f(a, BoolConst<true>{}); });
+  else with_act(act, [&](auto a) { f(a, BoolConst<false>{}); });
+}
+
 // Two FP32 -> two 16-bit values in one word (lo in the low half), round to nearest even.
 __device__ __forceinline__ uint32_t pack16(float lo, float hi, bool fp16) {
   if (fp16) {

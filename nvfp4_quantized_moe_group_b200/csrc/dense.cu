@@ -569,12 +569,13 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             }
           };
           fetch(32 * part);
-          with_act(p.act, [&](auto act) {
+          with_act(p.act, p.fp16 != 0, [&](auto act, auto fp16) {
 #pragma unroll 1
             for (int c = 32 * part; c < t.rows_valid; c += 64) {
               tmem_ld_wait();
               const PieceAt to{&map_out, &map_z, t.out_row + c, f0, t.rows_valid - c};
-              store_piece32<decltype(act)::value>(p, to, pieces, turn, v, bias, res, lane, [&] { fetch(c + 64); });
+              store_piece32<decltype(act)::value, decltype(fp16)::value>(p, to, pieces, turn, v, bias, res, lane,
+                                                                         [&] { fetch(c + 64); });
             }
           });
         }
@@ -874,7 +875,7 @@ mm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
         const float4 bias = p.bias != nullptr ? __ldg(reinterpret_cast<const float4*>(p.bias + col))
                                               : make_float4(0.f, 0.f, 0.f, 0.f);
         const int64_t at0 = t.out_row * (int64_t)p.J + col;
-        with_act(p.act, [&](auto act) {
+        with_act(p.act, p.fp16 != 0, [&](auto act, auto fp16) {
           // four rows at a time: their residual loads and the reads of the parts overlap
           for (int r0 = rank + split * q; r0 < t.rows_valid; r0 += 16 * split) {
             uint2 res[4];
@@ -901,7 +902,7 @@ mm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
                   v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
                 }
               }
-              store4<decltype(act)::value>(p, v, bias, res[i], at0 + r * (int64_t)p.J);
+              store4<decltype(act)::value, decltype(fp16)::value>(p, v, bias, res[i], at0 + r * (int64_t)p.J);
             }
           }
         });

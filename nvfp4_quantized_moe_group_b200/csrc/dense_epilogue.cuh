@@ -9,9 +9,8 @@
 namespace nvfp4moe {
 
 // Four consecutive output columns of one row; res: the residual's, already loaded (with p.residual).
-template <int kAct>
+template <int kAct, bool fp16>
 __device__ __forceinline__ void store4(const MmArgs& p, float4 f, float4 bias, uint2 res, int64_t at) {
-  const bool fp16 = p.fp16 != 0;
   float v[4] = {f.x + bias.x, f.y + bias.y, f.z + bias.z, f.w + bias.w};
   if (p.z_out != nullptr)
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.z_out) + at) =
@@ -96,11 +95,10 @@ struct PieceAt {
 // v: the accumulator's 32 x 32 values as two tmem_ld_16x256b_x4 give them; bias[b]: of feature 8 b + lane / 4;
 // res: this lane's residual vectors (rows lane / 4, + 8, + 16, + 24, features 8 (lane % 4) on).  pieces: the
 // warp's [2][y, z] pieces, used in turn.  next(): called once v and res have been used.
-template <int kAct, typename Next>
+template <int kAct, bool fp16, typename Next>
 __device__ __forceinline__ void store_piece32(const MmArgs& p, const PieceAt& to, uint8_t* pieces, int& turn,
                                               const uint32_t (*v)[16], const float* bias, const uint4* res, int lane,
                                               Next next) {
-  const bool fp16 = p.fp16 != 0;
   uint8_t* p_y = pieces + turn * 2 * kTokenPiece;
   uint8_t* p_z = p_y + kTokenPiece;
   turn ^= 1;
