@@ -577,7 +577,8 @@ enum {
  *            empty and need no alignment.  Rows outside offsets[0] .. offsets[E] are neither used nor
  *            written.  Offsets that break the rule raise NVFP4MOE_ERR_ARG in the status word; every
  *            segment then counts as empty.
- *   ws       nvfp4moe_grouped_mm_workspace_bytes(E) bytes
+ *   ws       nvfp4moe_grouped_mm_workspace_bytes(E) bytes, backward
+ *            nvfp4moe_grouped_mm_backward_workspace_bytes(M, K, E, N)
  *
  * nvfp4moe_grouped_mm_backward, with dy [M][N] the gradient of y:
  *   dx       out [M][K] or NULL: dx[i] = dy[i] W_e (rows outside the segments are not written)
@@ -589,6 +590,7 @@ NVFP4MOE_API size_t nvfp4moe_grouped_mm_workspace_bytes(int32_t E);
 NVFP4MOE_API int nvfp4moe_grouped_mm(int32_t dtype, const void* x, int64_t M, int32_t K, const void* w, int32_t E,
                                      int32_t N, const int32_t* offsets, void* y, void* ws, size_t ws_bytes,
                                      void* stream);
+NVFP4MOE_API size_t nvfp4moe_grouped_mm_backward_workspace_bytes(int64_t M, int32_t K, int32_t E, int32_t N);
 NVFP4MOE_API int nvfp4moe_grouped_mm_backward(int32_t dtype, const void* dy, const void* x, const void* w, int64_t M,
                                               int32_t K, int32_t E, int32_t N, const int32_t* offsets, void* dx,
                                               void* dw, int32_t dw_dtype, void* ws, size_t ws_bytes, void* stream);

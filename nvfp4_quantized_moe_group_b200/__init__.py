@@ -34,7 +34,8 @@ from ._lib import (  # noqa: F401
     forward_residual, status_read, last_device_status, workspace_bytes, quantize_fp8, Fp8Experts, forward_fp8, forward_fp8_workspace_bytes,
     forward_partial, finalize, amax, ep_dispatch, ep_dispatch_workspace_bytes, ep_experts, ep_experts_workspace_bytes,
     ep_combine, forward_partial_peer, ipc_handle, ipc_open, ipc_close,
-    grouped_mm, grouped_mm_backward, grouped_mm_workspace_bytes, linear, linear_backward, linear_workspace_bytes,
+    grouped_mm, grouped_mm_backward, grouped_mm_workspace_bytes, grouped_mm_backward_workspace_bytes,
+    linear, linear_backward, linear_workspace_bytes,
     linear_backward_workspace_bytes, layer_norm, layer_norm_backward, layer_norm_backward_workspace_bytes,
     status_string, last_launch_count, forward_workspace_bytes, route_workspace_bytes,
     quantize_workspace_bytes, swizzled_scale_bytes, declared_symbols, lib, LIB_PATH, StageTimer, STAGES,

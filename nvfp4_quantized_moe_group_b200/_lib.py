@@ -142,6 +142,7 @@ _SIGS = {
     "nvfp4moe_ep_experts": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _P, _P, _P, _SZ, _P]),
     "nvfp4moe_ep_combine": (ctypes.c_int, [_P, _P, _I64, ctypes.c_int32, ctypes.c_int32, _P, _P]),
     "nvfp4moe_grouped_mm_workspace_bytes": (_SZ, [ctypes.c_int32]),
+    "nvfp4moe_grouped_mm_backward_workspace_bytes": (_SZ, [_I64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32]),
     "nvfp4moe_grouped_mm": (ctypes.c_int, [ctypes.c_int32, _P, _I64, ctypes.c_int32, _P, ctypes.c_int32,
                                            ctypes.c_int32, _P, _P, _P, _SZ, _P]),
     "nvfp4moe_grouped_mm_backward": (ctypes.c_int, [ctypes.c_int32, _P, _P, _P, _I64, ctypes.c_int32, ctypes.c_int32,
@@ -855,6 +856,11 @@ def grouped_mm_workspace_bytes(E: int) -> int:
     return int(lib().nvfp4moe_grouped_mm_workspace_bytes(int(E)))
 
 
+@functools.lru_cache(maxsize=1024)
+def grouped_mm_backward_workspace_bytes(M: int, K: int, E: int, N: int) -> int:
+    return int(lib().nvfp4moe_grouped_mm_backward_workspace_bytes(int(M), int(K), int(E), int(N)))
+
+
 def grouped_mm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, out: torch.Tensor | None = None, ws=None,
                stream=None) -> torch.Tensor:
     """Products grouped by expert (nvfp4moe_grouped_mm): x [M, K] bf16 or fp16, w [E, N, K],
@@ -899,7 +905,7 @@ def grouped_mm_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, offs
     if dw is None and need_dw:
         dw = dy.new_empty((E, N, K), dtype=wt)
     if ws is None:
-        ws = _workspace(grouped_mm_workspace_bytes(E), dy.device)
+        ws = _workspace(grouped_mm_backward_workspace_bytes(M, K, E, N), dy.device)
     _check(lib().nvfp4moe_grouped_mm_backward(DTYPES[dt], _ptr(dy), _ptr(x), _ptr(w), M, K, E, N, _ptr(offsets),
                                               _ptr(dx), _ptr(dw), DTYPES[wt], _ptr(ws), ws.numel(), _stream(stream)),
            "nvfp4moe_grouped_mm_backward")

@@ -405,44 +405,59 @@ struct ProductWs {
   CUtensorMap* maps;       // grouped calls only
   uint16_t* dz;            // linear_backward only
   float* partials;
+  float* row_parts;        // parts of the row product (forward or dgrad) and of wgrad, where they are split
+  float* wgrad_parts;
   size_t bytes;
 };
 
-ProductWs carve_product(void* ws, int32_t E) {
+// Floats of the parts of a row product [M][J] run as `plan`, and of a weight gradient [E][I][J].
+size_t row_part_floats(const MmPlan& plan, int64_t M, int32_t J) {
+  return plan.pair && plan.split > 1 ? (size_t)plan.split * (size_t)(M * J) : 0;
+}
+size_t wgrad_part_floats(int split, int32_t E, int32_t I, int32_t J) {
+  return split > 1 ? (size_t)split * (size_t)E * (size_t)((int64_t)I * J) : 0;
+}
+
+ProductWs carve_product(void* ws, int32_t E, size_t row_floats, size_t wgrad_floats) {
   Carver c(ws);
   ProductWs p{};
   p.hdr = c.take<WsHeader>(1);
   p.seg = c.take<int32_t>(2 * (size_t)E);
   p.tiles = c.take<int32_t>((size_t)E + 1);
   p.maps = c.take<CUtensorMap>(2 * (size_t)E);
+  p.row_parts = c.take<float>(row_floats);
+  p.wgrad_parts = c.take<float>(wgrad_floats);
   p.bytes = c.off;
   return p;
 }
 
-ProductWs carve_linear_backward(void* ws, int64_t M, int32_t N) {
+ProductWs carve_linear_backward(void* ws, int64_t M, int32_t N, size_t row_floats, size_t wgrad_floats) {
   Carver c(ws);
   ProductWs p{};
   p.hdr = c.take<WsHeader>(1);
   p.dz = c.take<uint16_t>((size_t)(M * N));
   p.partials = c.take<float>((size_t)act_grad_partials(M, N) * (size_t)N);
+  p.row_parts = c.take<float>(row_floats);
+  p.wgrad_parts = c.take<float>(wgrad_floats);
   p.bytes = c.off;
   return p;
 }
 
 // Resets the status word and builds the segment table of a ragged call (offsets != nullptr).
-// J, R: the columns and reduction length of the call's row product (forward or dgrad).
-// wgrad: its operands, when the call runs a ragged one.
-cudaError_t start_product(const ProductWs& p, const int32_t* offsets, int E, int64_t M, int J, int R,
+// plan: of the call's row product (forward or dgrad).  wgrad: its operands, when the call runs a ragged one.
+cudaError_t start_product(const ProductWs& p, const int32_t* offsets, int E, int64_t M, const MmPlan& plan,
                           const MmWgradOperands* wgrad, cudaStream_t s) {
   g_last_status = p.hdr;
-  const int tile_rows = mm_plan(M, E, J, R, offsets != nullptr).tile_rows;
-  const cudaError_t e = launch_mm_table(offsets, E, M, tile_rows, MmTable{p.seg, p.tiles, p.maps}, p.hdr, wgrad, s);
+  const cudaError_t e = launch_mm_table(offsets, E, M, plan.tile_rows, MmTable{p.seg, p.tiles, p.maps}, p.hdr, wgrad, s);
   if (e == cudaSuccess) ++g_launches;
   return e;
 }
 
-MmArgs product_args(const ProductWs& p, bool ragged, int E, int64_t M, int32_t dtype) {
+MmArgs product_args(const ProductWs& p, bool ragged, int E, int64_t M, int32_t dtype, const MmPlan& plan) {
   MmArgs m{};
+  m.plan = plan;
+  m.split = plan.pair ? plan.split : 1;
+  m.parts = p.row_parts;
   m.seg = ragged ? p.seg : nullptr;
   m.tiles = ragged ? p.tiles : nullptr;
   m.seg_maps = ragged ? p.maps : nullptr;
@@ -455,16 +470,18 @@ MmArgs product_args(const ProductWs& p, bool ragged, int E, int64_t M, int32_t d
 }
 
 // dx = dy W (per segment) and dw = dy^T x, either of them when asked for.  base.late_wait: for the
-// first of them; the second never depends on the first.
-cudaError_t product_gradients(const ProductWs& p, const MmArgs& base, const void* dy, const void* x, const void* w, int32_t K, int32_t N,
-                              void* dx, void* dw, int32_t dw_dtype, cudaStream_t s) {
+// first of them; the second never depends on the first, and their joins come after both.
+cudaError_t product_gradients(const ProductWs& p, const MmArgs& base, const void* dy, const void* x, const void* w,
+                              int32_t K, int32_t N, void* dx, void* dw, int32_t dw_dtype, int wgrad_split,
+                              cudaStream_t s) {
   cudaError_t e = cudaSuccess;
-  if (dx != nullptr && base.rows > 0) {
-    MmArgs m = base;
-    m.J = K;
-    m.R = N;
-    m.out = dx;
-    e = launch_mm(kMmDgrad, dy, w, m, s);
+  MmArgs d = base;
+  d.J = K;
+  d.R = N;
+  d.out = dx;
+  const bool rows = dx != nullptr && base.rows > 0;
+  if (rows) {
+    e = launch_mm(kMmDgrad, dy, w, d, s);
     if (e != cudaSuccess) return e;
     ++g_launches;
   }
@@ -476,9 +493,21 @@ cudaError_t product_gradients(const ProductWs& p, const MmArgs& base, const void
     m.J = K;
     m.out = dw;
     m.out_f32 = dw_dtype == NVFP4MOE_FP32;
+    m.split = wgrad_split;
+    m.parts = p.wgrad_parts;
     m.work_counter = &p.hdr->work[1];
-    m.late_wait = base.late_wait || dx != nullptr;
+    m.late_wait = base.late_wait || rows;
     e = launch_mm(kMmWgrad, dy, x, m, s);
+    if (e != cudaSuccess) return e;
+    ++g_launches;
+    if (wgrad_split > 1) {
+      e = launch_mm_join(kMmWgrad, m, s);
+      if (e != cudaSuccess) return e;
+      ++g_launches;
+    }
+  }
+  if (rows && d.split > 1) {
+    e = launch_mm_join(kMmDgrad, d, s);
     if (e == cudaSuccess) ++g_launches;
   }
   return e;
@@ -1682,7 +1711,7 @@ int nvfp4moe_ep_combine(const float* rows, const int32_t* send_pos, int64_t T, i
 }
 
 size_t nvfp4moe_grouped_mm_workspace_bytes(int32_t E) {
-  return E < 1 || E > kMaxGroups ? 0 : carve_product(nullptr, E).bytes;
+  return E < 1 || E > kMaxGroups ? 0 : carve_product(nullptr, E, 0, 0).bytes;
 }
 
 int nvfp4moe_grouped_mm(int32_t dtype, const void* x, int64_t M, int32_t K, const void* w, int32_t E, int32_t N,
@@ -1694,20 +1723,26 @@ int nvfp4moe_grouped_mm(int32_t dtype, const void* x, int64_t M, int32_t K, cons
     return NVFP4MOE_ERR_ARG;
   if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, 16) || !aligned(offsets, 4) || !aligned(ws, kAlign))
     return NVFP4MOE_ERR_ARG;
-  const ProductWs p = carve_product(ws, E);
+  const ProductWs p = carve_product(ws, E, 0, 0);
   if (ws_bytes < p.bytes) return NVFP4MOE_ERR_WORKSPACE;
   const int st = check_device();
   if (st != NVFP4MOE_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (start_product(p, offsets, E, M, N, K, nullptr, s) != cudaSuccess) return cuda_failed();
+  const MmPlan plan = mm_plan(M, E, N, K, true);
+  if (start_product(p, offsets, E, M, plan, nullptr, s) != cudaSuccess) return cuda_failed();
   if (M == 0) return NVFP4MOE_OK;
-  MmArgs m = product_args(p, true, E, M, dtype);
+  MmArgs m = product_args(p, true, E, M, dtype, plan);
   m.J = N;
   m.R = K;
   m.out = y;
   if (launch_mm(kMmForward, x, w, m, s) != cudaSuccess) return cuda_failed();
   ++g_launches;
   return NVFP4MOE_OK;
+}
+
+size_t nvfp4moe_grouped_mm_backward_workspace_bytes(int64_t M, int32_t K, int32_t E, int32_t N) {
+  if (!product_shape(M, K, N, E)) return 0;
+  return carve_product(nullptr, E, 0, wgrad_part_floats(mm_wgrad_split(M, E, N, K), E, N, K)).bytes;
 }
 
 int nvfp4moe_grouped_mm_backward(int32_t dtype, const void* dy, const void* x, const void* w, int64_t M, int32_t K,
@@ -1722,21 +1757,25 @@ int nvfp4moe_grouped_mm_backward(int32_t dtype, const void* dy, const void* x, c
   if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(w, 16) || !aligned(dx, 16) || !aligned(dw, 16) ||
       !aligned(offsets, 4) || !aligned(ws, kAlign))
     return NVFP4MOE_ERR_ARG;
-  const ProductWs p = carve_product(ws, E);
+  const int split = mm_wgrad_split(M, E, N, K);
+  const ProductWs p = carve_product(ws, E, 0, wgrad_part_floats(split, E, N, K));
   if (ws_bytes < p.bytes) return NVFP4MOE_ERR_WORKSPACE;
   const int st = check_device();
   if (st != NVFP4MOE_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const MmWgradOperands wgrad{dy, x, N, K};
-  if (start_product(p, offsets, E, M, K, N, dw != nullptr && M > 0 ? &wgrad : nullptr, s) != cudaSuccess)
+  const MmPlan plan = mm_plan(M, E, K, N, true);
+  if (start_product(p, offsets, E, M, plan, dw != nullptr && M > 0 ? &wgrad : nullptr, s) != cudaSuccess)
     return cuda_failed();
-  if (product_gradients(p, product_args(p, true, E, M, dtype), dy, x, w, K, N, dx, dw, dw_dtype, s) != cudaSuccess)
+  if (product_gradients(p, product_args(p, true, E, M, dtype, plan), dy, x, w, K, N, dx, dw, dw_dtype, split, s) !=
+      cudaSuccess)
     return cuda_failed();
   return NVFP4MOE_OK;
 }
 
 size_t nvfp4moe_linear_workspace_bytes(int64_t M, int32_t K, int32_t N) {
-  return product_shape(M, K, N, 1) ? carve_product(nullptr, 1).bytes : 0;
+  if (!product_shape(M, K, N, 1)) return 0;
+  return carve_product(nullptr, 1, row_part_floats(mm_plan(M, 1, N, K, false), M, N), 0).bytes;
 }
 
 int nvfp4moe_linear(int32_t dtype, const void* x, int64_t M, int32_t K, const void* w, int32_t N, const float* bias,
@@ -1748,14 +1787,15 @@ int nvfp4moe_linear(int32_t dtype, const void* x, int64_t M, int32_t K, const vo
   if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, 16) || !aligned(bias, 16) || !aligned(residual, 16) ||
       !aligned(z_out, 16) || !aligned(ws, kAlign))
     return NVFP4MOE_ERR_ARG;
-  const ProductWs p = carve_product(ws, 1);
+  const MmPlan plan = mm_plan(M, 1, N, K, false);
+  const ProductWs p = carve_product(ws, 1, row_part_floats(plan, M, N), 0);
   if (ws_bytes < p.bytes) return NVFP4MOE_ERR_WORKSPACE;
   const int st = check_device();
   if (st != NVFP4MOE_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (start_product(p, nullptr, 1, M, N, K, nullptr, s) != cudaSuccess) return cuda_failed();
+  if (start_product(p, nullptr, 1, M, plan, nullptr, s) != cudaSuccess) return cuda_failed();
   if (M == 0) return NVFP4MOE_OK;
-  MmArgs m = product_args(p, false, 1, M, dtype);
+  MmArgs m = product_args(p, false, 1, M, dtype, plan);
   m.J = N;
   m.R = K;
   m.out = y;
@@ -1765,11 +1805,18 @@ int nvfp4moe_linear(int32_t dtype, const void* x, int64_t M, int32_t K, const vo
   m.z_out = z_out;
   if (launch_mm(kMmForward, x, w, m, s) != cudaSuccess) return cuda_failed();
   ++g_launches;
+  if (m.split > 1) {
+    if (launch_mm_join(kMmForward, m, s) != cudaSuccess) return cuda_failed();
+    ++g_launches;
+  }
   return NVFP4MOE_OK;
 }
 
 size_t nvfp4moe_linear_backward_workspace_bytes(int64_t M, int32_t K, int32_t N) {
-  return product_shape(M, K, N, 1) ? carve_linear_backward(nullptr, M, N).bytes : 0;
+  if (!product_shape(M, K, N, 1)) return 0;
+  return carve_linear_backward(nullptr, M, N, row_part_floats(mm_plan(M, 1, K, N, false), M, K),
+                               wgrad_part_floats(mm_wgrad_split(M, 1, N, K), 1, N, K))
+      .bytes;
 }
 
 int nvfp4moe_linear_backward(int32_t dtype, const void* dy, const void* x, const void* w, const void* z, int64_t M,
@@ -1787,7 +1834,10 @@ int nvfp4moe_linear_backward(int32_t dtype, const void* dy, const void* x, const
   if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(w, 16) || !aligned(z, 16) || !aligned(dx, 16) ||
       !aligned(dw, 16) || !aligned(db, 4) || !aligned(ws, kAlign))
     return NVFP4MOE_ERR_ARG;
-  const ProductWs p = carve_linear_backward(ws, M, N);
+  const MmPlan plan = mm_plan(M, 1, K, N, false);
+  const int split = mm_wgrad_split(M, 1, N, K);
+  const ProductWs p =
+      carve_linear_backward(ws, M, N, row_part_floats(plan, M, K), wgrad_part_floats(split, 1, N, K));
   if (ws_bytes < p.bytes) return NVFP4MOE_ERR_WORKSPACE;
   const int st = check_device();
   if (st != NVFP4MOE_OK) return st;
@@ -1797,16 +1847,16 @@ int nvfp4moe_linear_backward(int32_t dtype, const void* dy, const void* x, const
     if (launch_act_grad(dy, z, M, N, act, dtype == NVFP4MOE_FP16, p.dz, db, p.partials, p.hdr, &g_launches, s) !=
         cudaSuccess)
       return cuda_failed();
-  } else if (start_product(p, nullptr, 1, M, N, K, nullptr, s) != cudaSuccess) {
+  } else if (start_product(p, nullptr, 1, M, plan, nullptr, s) != cudaSuccess) {
     return cuda_failed();
   }
   if (M == 0 && db != nullptr && cudaMemsetAsync(db, 0, (size_t)N * sizeof(float), s) != cudaSuccess)
     return cuda_failed();
   const void* dz = act != NVFP4MOE_ACT_NONE ? p.dz : dy;
-  MmArgs m = product_args(p, false, 1, M, dtype);
+  MmArgs m = product_args(p, false, 1, M, dtype, plan);
   // with db the kernel before is the sum of its partials, which dz's has finished before
   m.late_wait = db != nullptr;
-  if (product_gradients(p, m, dz, x, w, K, N, dx, dw, dw_dtype, s) != cudaSuccess) return cuda_failed();
+  if (product_gradients(p, m, dz, x, w, K, N, dx, dw, dw_dtype, split, s) != cudaSuccess) return cuda_failed();
   return NVFP4MOE_OK;
 }
 

@@ -190,14 +190,15 @@ struct Tile {
   int a0, b0;        // kMmWgrad: first i, first j; else first token row, first j
   int64_t out_row;   // row of D (in the whole output) that a0 is
   int rows_valid;    // rows of the tile to store
-  int steps;         // 64-deep reduction steps
+  int out_e;         // matrix of the output (or of its parts) that the tile belongs to
+  int k0, steps;     // first 64-deep reduction step and how many
 };
 
 template <int kMode>
 __device__ __forceinline__ int total_tiles(const MmArgs& p, int tile_i, int tile_j) {
   const int ntj = (p.J + tile_j - 1) / tile_j;
-  if constexpr (kMode == kMmWgrad) return p.E * ((p.I + tile_i - 1) / tile_i) * ntj;
-  return (p.tiles != nullptr ? p.tiles[p.E] : (int)((p.rows + tile_i - 1) / tile_i)) * ntj;
+  if constexpr (kMode == kMmWgrad) return p.split * p.E * ((p.I + tile_i - 1) / tile_i) * ntj;
+  return (p.tiles != nullptr ? p.tiles[p.E] : p.split * (int)((p.rows + tile_i - 1) / tile_i)) * ntj;
 }
 
 // Tile w in expert-major order; within an expert, blocks of kRasterRows row tiles go through the
@@ -207,12 +208,14 @@ template <int kMode>
 __device__ __forceinline__ Tile tile_at(const MmArgs& p, int w, int tile_i, int tile_j) {
   Tile t;
   const int ntj = (p.J + tile_j - 1) / tile_j;
-  int mt_e, local, seg_row = 0;
+  int mt_e, local, seg_row = 0, part = 0;
   int64_t seg_rows = p.rows;
   if constexpr (kMode == kMmWgrad) {
     mt_e = (p.I + tile_i - 1) / tile_i;
-    t.e = w / (mt_e * ntj);
-    local = w - t.e * mt_e * ntj;
+    t.out_e = w / (mt_e * ntj);
+    local = w - t.out_e * mt_e * ntj;
+    part = t.out_e / p.E;
+    t.e = t.out_e - part * p.E;
   } else if (p.tiles != nullptr) {
     int lo = 0, hi = p.E;
     while (hi - lo > 1) {
@@ -220,12 +223,15 @@ __device__ __forceinline__ Tile tile_at(const MmArgs& p, int w, int tile_i, int 
       if (p.tiles[mid] * ntj <= w) lo = mid; else hi = mid;
     }
     t.e = lo;
+    t.out_e = 0;
     mt_e = p.tiles[lo + 1] - p.tiles[lo];
     local = w - p.tiles[lo] * ntj;
   } else {
     t.e = 0;
     mt_e = (int)((p.rows + tile_i - 1) / tile_i);
-    local = w;
+    part = w / (mt_e * ntj);
+    t.out_e = part;
+    local = w - part * mt_e * ntj;
   }
   if (p.seg != nullptr) {
     // wgrad may have started before its stream's previous kernel ended, so without the wait that makes
@@ -255,6 +261,11 @@ __device__ __forceinline__ Tile tile_at(const MmArgs& p, int w, int tile_i, int 
     t.out_row = t.a0;
     t.rows_valid = left < share ? (int)left : (int)share;
     t.steps = (p.R + kBK - 1) / kBK;
+  }
+  t.k0 = 0;
+  if (p.split > 1) {                         // at most 2^19 steps and 74 parts
+    t.k0 = t.steps * part / p.split;
+    t.steps = t.steps * (part + 1) / p.split - t.k0;
   }
   return t;
 }
@@ -364,7 +375,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
   pdl_trigger();
 
   const uint32_t tmem = s.tmem_base;
-  const int tile_i = kTokens ? p.tile_rows : kPairTile;
+  const int tile_i = kTokens ? p.plan.tile_rows : kPairTile;
   const int total = total_tiles<kMode>(p, tile_i, kPairTile);
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
@@ -430,7 +441,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
           }
           const uint32_t bar = map_rank(smem_u32(&s.full[stage]), 0);
           if (rank == 0) mbar_arrive_expect_tx(&s.full[stage], 2 * (kOperandBytes + b_bytes));
-          const int r = k * kBK;
+          const int r = (t.k0 + k) * kBK;
           const int ae = kTokens ? t.e : 0;
           if constexpr (kAMn) {
             tma_load_pair(s.a[stage], ma, bar, ai, r, ae);
@@ -539,7 +550,19 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
       const int lane0 = (int)rank * kHalf + q * 32;        // this warp's first accumulator lane in the tile
       // the warps of a quarter take its 32-column pieces in turn
       if constexpr (kTokens) {
-        if (t.b0 + lane0 < p.J) {
+        if (p.parts != nullptr) {              // sums of a part: FP32, a feature per lane
+          const int f = t.b0 + lane0 + lane;
+#pragma unroll 1
+          for (int c = 32 * part; c < t.rows_valid; c += 64) {
+            uint32_t v[32];
+            tmem_ld_32x32b_x32(acc + c, v);
+            tmem_ld_wait();
+            float* to = p.parts + ((int64_t)t.out_e * p.rows + t.out_row + c) * p.J + f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (f < p.J && c + i < t.rows_valid) to[(int64_t)i * p.J] = __uint_as_float(v[i]);
+          }
+        } else if (t.b0 + lane0 < p.J) {
           const int f0 = t.b0 + lane0;
           const bool col_ok = f0 + (lane & 3) * 8 < p.J;      // J is a multiple of 8
           float bias[4];
@@ -606,14 +629,14 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
           // rows and columns behind the output's are clipped by the map
           if (lane0 >= t.rows_valid || col >= p.J) continue;
           if (p.out_f32) {
-            store_piece(&map_out, pieces, turn, v[j], col, row, t.e, lane);
-            if (col + 32 < p.J) store_piece(&map_out, pieces, turn, v[j] + 32, col + 32, row, t.e, lane);
+            store_piece(&map_out, pieces, turn, v[j], col, row, t.out_e, lane);
+            if (col + 32 < p.J) store_piece(&map_out, pieces, turn, v[j] + 32, col + 32, row, t.out_e, lane);
           } else {
             uint32_t h[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               h[i] = pack16(__uint_as_float(v[j][2 * i]), __uint_as_float(v[j][2 * i + 1]), p.fp16 != 0);
-            store_piece(&map_out, pieces, turn, h, col, row, t.e, lane);
+            store_piece(&map_out, pieces, turn, h, col, row, t.out_e, lane);
           }
         }
       }
@@ -992,14 +1015,24 @@ __global__ void __launch_bounds__(kMaxGroups) mm_table_kernel(const int32_t* off
 }
 
 template <int kMode>
-cudaError_t launch_pair(const void* a, const void* b, const MmArgs& args, int tile_rows, cudaStream_t stream) {
+cudaError_t launch_pair(const void* a, const void* b, const MmArgs& args, cudaStream_t stream) {
   MmArgs m = args;
-  m.tile_rows = tile_rows;
+  if (m.split <= 1) {
+    m.split = 1;
+    m.parts = nullptr;
+  } else if (m.parts == nullptr || (kMode != kMmWgrad && m.seg != nullptr)) {
+    return cudaErrorInvalidValue;
+  }
+  if (kMode == kMmWgrad && m.split > 1) {
+    m.out = m.parts;
+    m.out_f32 = 1;
+  }
+  const int tile_rows = m.plan.tile_rows;
   CUtensorMap map_a, map_b, map_b64, map_b32, map_out, map_z;
   int err;
   if (kMode == kMmWgrad) {
     err = make_tma_16(&map_a, a, m.I, m.rows, 1, kBK) | make_tma_16(&map_b, b, m.J, m.rows, 1, kBK) |
-          make_tma_3d(&map_out, m.out, m.out_f32 ? 4 : 2, m.J, m.I, m.E, 32, 128);
+          make_tma_3d(&map_out, m.out, m.out_f32 ? 4 : 2, m.J, m.I, (uint64_t)m.split * m.E, 32, 128);
     map_b64 = map_b32 = map_z = map_b;                 // not used
   } else {
     err = kMode == kMmForward ? make_tma_16(&map_a, b, m.R, m.J, m.E, kHalf)
@@ -1019,7 +1052,7 @@ cudaError_t launch_pair(const void* a, const void* b, const MmArgs& args, int ti
   const int64_t ntj = (m.J + kPairTile - 1) / kPairTile;
   int64_t most = kMode == kMmWgrad ? (int64_t)m.E * ((m.I + kPairTile - 1) / kPairTile)
                                    : (m.rows + tile_rows - 1) / tile_rows + (m.seg != nullptr ? m.E : 0);
-  most *= ntj;
+  most *= ntj * m.split;
   const int64_t pairs = num_sms() / 2;
   return launch_pdl(mm_pair_kernel<kMode>, dim3((unsigned)(2 * (most < pairs ? most : pairs))), dim3(kPairThreads),
                     smem, stream, map_a, map_b, map_b64, map_b32, map_out, map_z, m);
@@ -1060,15 +1093,48 @@ cudaError_t launch_narrow(const void* a, const void* b, const MmArgs& m, int spl
 
 template <int kMode>
 cudaError_t launch_rows(const void* a, const void* b, const MmArgs& m, cudaStream_t stream) {
-  const MmPlan plan = mm_plan(m.rows, m.E, m.J, m.R, m.seg != nullptr);
-  if (plan.pair) return launch_pair<kMode>(a, b, m, plan.tile_rows, stream);
-  switch (plan.tile_rows) {
-    case 16: return launch_narrow<kMode, 16>(a, b, m, plan.split, stream);
-    case 32: return launch_narrow<kMode, 32>(a, b, m, plan.split, stream);
-    case 64: return launch_narrow<kMode, 64>(a, b, m, plan.split, stream);
-    default: return launch_narrow<kMode, 128>(a, b, m, plan.split, stream);
+  if (m.plan.pair) return launch_pair<kMode>(a, b, m, stream);
+  switch (m.plan.tile_rows) {
+    case 16: return launch_narrow<kMode, 16>(a, b, m, m.plan.split, stream);
+    case 32: return launch_narrow<kMode, 32>(a, b, m, m.plan.split, stream);
+    case 64: return launch_narrow<kMode, 64>(a, b, m, m.plan.split, stream);
+    default: return launch_narrow<kMode, 128>(a, b, m, m.plan.split, stream);
   }
 }
+
+// Four neighbouring values a thread: the parts' sums in their order, then the product's epilogue.  At
+// most 74 tiles' parts, which are in L2: its time is its latency.
+constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads) mm_join_kernel(const __grid_constant__ MmArgs p, int n4) {
+  pdl_wait();
+  pdl_trigger();
+  const int at = blockIdx.x * kJoinThreads + threadIdx.x;
+  if (at >= n4) return;
+  const int col = at % (p.J / 4) * 4;
+  const float4* from = reinterpret_cast<const float4*>(p.parts) + at;
+  uint2 res = make_uint2(0, 0);
+  if (p.residual != nullptr) res = static_cast<const uint2*>(p.residual)[at];
+  const float4 bias = p.bias != nullptr ? __ldg(reinterpret_cast<const float4*>(p.bias + col))
+                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int i = 0; i < p.split; ++i) {
+    const float4 o = __ldcg(from + (int64_t)i * n4);
+    v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+  }
+  if (p.out_f32) {
+    static_cast<float4*>(p.out)[at] = v;
+    return;
+  }
+  with_act(p.act, p.fp16 != 0, [&](auto act, auto fp16) {
+    store4<decltype(act)::value, decltype(fp16)::value>(p, v, bias, res, (int64_t)at * 4);
+  });
+}
+
+// Where pairs share reductions: at most this many tiles of parts, one for each pair.
+constexpr int kPairs = 74;
+// SM clocks of the launch that joins `split` parts of n values, and of writing them.
+double join_cost(int split, double n) { return 5000.0 + split * n * 8.0 / 2500.0; }
 
 }  // namespace
 
@@ -1089,14 +1155,18 @@ MmPlan mm_plan(int64_t rows, int E, int J, int R, bool ragged) {
   auto consider = [&](bool pair, int tile, int split) {
     const int64_t per_seg = (mean + tile - 1) / tile, cols = pair ? kPairTile : kHalf;
     const int64_t tiles = busy * per_seg * ((J + cols - 1) / cols);
-    const int64_t room = pair ? 74 : clusters_that_fit(split);
-    const int64_t waves = (tiles + room - 1) / room;
+    if (pair && split > 1 && tiles * split > kPairs) return;
+    const int64_t room = pair ? kPairs : clusters_that_fit(split);
+    const int64_t waves = pair && split > 1 ? 1 : (tiles + room - 1) / room;
     const double n = pair ? (double)(((mean + per_seg - 1) / per_seg + 31) / 32 * 32) : (double)tile;
     double step = (16384.0 + (pair ? 64.0 : 128.0) * n) / 45.0;
     if (step < 2.0 * n) step = 2.0 * n;
-    double cost = (double)waves * (double)((steps + split - 1) / split) * step;
+    const double mma = (double)((steps + split - 1) / split) * step;
+    const double epilogue = pair ? 2300.0 + 14.0 * n : 1900.0 + 68.0 * n;
+    double cost = mma + (double)(waves - 1) * (mma > epilogue ? mma : epilogue);
     if (cost < hbm) cost = hbm;
-    cost += pair ? 4000.0 + 12.0 * n : 2500.0 + 25.0 * n + (split > 1 ? (600.0 + 8.0 * n) * (double)waves : 0.0);
+    cost += pair ? 4000.0 + 12.0 * n + (split > 1 ? join_cost(split, (double)rows * J) : 0.0)
+                 : 2500.0 + 25.0 * n + (split > 1 ? (600.0 + 8.0 * n) * (double)waves : 0.0);
     if (cost < best_cost) {
       best_cost = cost;
       best = MmPlan{pair, tile, split};
@@ -1107,6 +1177,34 @@ MmPlan mm_plan(int64_t rows, int E, int J, int R, bool ragged) {
     for (int split = 1; split <= kMaxSplit && split * 4 <= (steps > 4 ? steps : 4); ++split) consider(false, tile, split);
   }
   for (int tile = kPairTile; tile >= 64; tile -= 32) consider(true, tile, 1);
+  // (mean <= 2^25 rows: past 74 tiles nothing is shared)
+  if (!ragged && mean <= kPairs * kPairTile)
+    for (int tile = kPairTile; tile >= 64; tile -= 32) {
+      const int64_t tiles = (mean + tile - 1) / tile * ((J + kPairTile - 1) / kPairTile);
+      // the most parts that fit, and half as many
+      for (int64_t split = kPairs / tiles < steps / 4 ? kPairs / tiles : steps / 4, i = 0; i < 2 && split > 1;
+           ++i, split /= 2)
+        consider(true, tile, (int)split);
+    }
+  return best;
+}
+
+// The rows' steps of a tile of wgrad run on one pair, in 2 * 256 clocks each at best (728 with the operands
+// brought in); parts of them on the pairs that would have no tile, when that saves more than the join costs.
+int mm_wgrad_split(int64_t rows, int E, int I, int J) {
+  const int64_t tiles = (int64_t)E * ((I + kPairTile - 1) / kPairTile) * ((J + kPairTile - 1) / kPairTile);
+  const int64_t steps = (rows + (int64_t)E * kBK - 1) / ((int64_t)E * kBK);   // of a segment, on average
+  int best = 1;
+  double best_cost = 728.0 * (double)steps;
+  for (int64_t split = kPairs / tiles < steps / 4 ? kPairs / tiles : steps / 4, i = 0; i < 2 && split > 1;
+       ++i, split /= 2) {
+    const double cost =
+        728.0 * (double)((steps + split - 1) / split) + join_cost((int)split, (double)E * (double)I * (double)J);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = (int)split;
+    }
+  }
   return best;
 }
 
@@ -1130,8 +1228,14 @@ cudaError_t launch_mm(int mode, const void* a, const void* b, const MmArgs& m, c
   switch (mode) {
     case kMmForward: return launch_rows<kMmForward>(a, b, m, stream);
     case kMmDgrad: return launch_rows<kMmDgrad>(a, b, m, stream);
-    default: return launch_pair<kMmWgrad>(a, b, m, kPairTile, stream);
+    default: return launch_pair<kMmWgrad>(a, b, m, stream);
   }
+}
+
+cudaError_t launch_mm_join(int mode, const MmArgs& m, cudaStream_t stream) {
+  const int64_t n4 = (mode == kMmWgrad ? (int64_t)m.E * m.I : m.rows) * m.J / 4;
+  return launch_pdl(mm_join_kernel, dim3((unsigned)((n4 + kJoinThreads - 1) / kJoinThreads)), dim3(kJoinThreads), 0,
+                    stream, m, (int)n4);
 }
 
 }  // namespace nvfp4moe

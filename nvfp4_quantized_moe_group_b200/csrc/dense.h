@@ -42,6 +42,18 @@ struct MmSegMaps {
   CUtensorMap* out;      // nullptr: none
 };
 
+// How forward and dgrad run: on CTA pairs with tiles of up to tile_rows token rows (a multiple of 32 up
+// to 256), or on single CTAs with tiles of tile_rows (16, 32, 64, 128), `split` CTAs or pairs sharing a tile's
+// reduction.  J output columns, R the reduction length.
+struct MmPlan {
+  bool pair;
+  int tile_rows;
+  int split;
+};
+MmPlan mm_plan(int64_t rows, int E, int J, int R, bool ragged);
+// In how many parts wgrad's pairs share the token rows (of each segment) of a tile.
+int mm_wgrad_split(int64_t rows, int E, int I, int J);
+
 struct MmArgs {
   const int32_t* seg;    // as in MmTable; nullptr: one segment, all `rows` rows
   const int32_t* tiles;
@@ -66,18 +78,11 @@ struct MmArgs {
                          // loads would see earlier kernels' writes only after the wait.
   int* work_counter;     // pairs; zero at launch: tiles handed out beyond the first of each CTA pair
                          // (nullptr: fixed turns, for tiles of one cost)
-  int tile_rows;         // pairs: most token rows of a tile (set by launch_mm)
+  MmPlan plan;           // forward, dgrad
+  int split;             // pairs: parts of a tile's reduction (forward, dgrad: plan.split, dense calls only)
+  float* parts;          // with split > 1: [split][rows][J], wgrad [split][E][I][J], the parts' sums; launch_mm_join
+                         // then finishes the product
 };
-
-// How forward and dgrad run: on CTA pairs with tiles of up to tile_rows token rows (a multiple of 32 up
-// to 256), or on single CTAs with tiles of tile_rows (16, 32, 64, 128), `split` CTAs sharing a tile's
-// reduction.  J output columns, R the reduction length.
-struct MmPlan {
-  bool pair;
-  int tile_rows;
-  int split;
-};
-MmPlan mm_plan(int64_t rows, int E, int J, int R, bool ragged);
 
 // Zeroes the status word and the work counters and, with offsets, checks them and writes the segment table for row
 // tiles of tile_rows.  Offsets that decrease or leave 0 .. rows raise kStatusBadInput and leave
@@ -87,6 +92,8 @@ cudaError_t launch_mm_table(const int32_t* offsets, int E, int64_t rows, int til
                             WsHeader* hdr, const MmWgradOperands* w, cudaStream_t stream);
 // The product.  a, b: the operands' base addresses.
 cudaError_t launch_mm(int mode, const void* a, const void* b, const MmArgs& m, cudaStream_t stream);
+// Adds the parts of a product of split > 1 in their order and finishes it: epilogue, rounding, store.
+cudaError_t launch_mm_join(int mode, const MmArgs& m, cudaStream_t stream);
 
 // dz = dy act'(z) (16 bit, written when act is not NONE) and db[n] = sum_m dy act'(z) (FP32, when
 // db is not nullptr; partials: act_grad_partials(M, N) * N floats).  Resets the workspace header as

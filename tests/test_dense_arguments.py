@@ -155,6 +155,12 @@ def test_norm_arguments(lib):
 def test_workspace_sizes(lib):
     assert moe.grouped_mm_workspace_bytes(0) == 0 and moe.grouped_mm_workspace_bytes(1025) == 0
     assert 256 < moe.grouped_mm_workspace_bytes(1) <= moe.grouped_mm_workspace_bytes(1024) < 1 << 20
+    # backward: parts of dw where few tiles have many rows
+    assert moe.grouped_mm_backward_workspace_bytes(64, 64, 4, 128) == moe.grouped_mm_workspace_bytes(4)
+    assert moe.grouped_mm_backward_workspace_bytes(1 << 20, 64, 1, 128) >= 2 * 4 * 64 * 128
+    assert moe.grouped_mm_backward_workspace_bytes((1 << 25) - 1, 256, 74, 256) < 1 << 27
+    assert moe.grouped_mm_backward_workspace_bytes(0, 64, 0, 128) == 0
+    assert moe.grouped_mm_backward_workspace_bytes(1 << 25, 64, 1, 128) == 0
     assert moe.linear_workspace_bytes(16, 64, 128) >= 256 and moe.linear_workspace_bytes(16, 65, 128) == 0
     assert moe.linear_backward_workspace_bytes(1000, 64, 128) >= 1000 * 128 * 2
     assert moe.linear_backward_workspace_bytes(-1, 64, 128) == 0

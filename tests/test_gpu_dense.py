@@ -69,6 +69,9 @@ GROUPED = [
     ([17] * 40, 24, 1000, 0, 0),
     ([2, 0] * 100, 128, 256, 0, 0),
     ([1025, 511], 320, 776, 7, 0),
+    # many rows, few tiles: dw's rows in parts
+    ([4000, 0], 264, 264, 2, 3),
+    ([3700, 0, 5, 1300, 64], 72, 40, 0, 0),
 ]
 
 
@@ -89,7 +92,7 @@ def test_grouped_forward_and_gradients(case, dtype):
     xd, wd, dyd, o = x.cuda(), w.cuda(), dy.cuda(), dev_offsets(off)
     inside = slice(before, off[-1])
     out = torch.full((M, N), 7.0, dtype=dtype, device="cuda")
-    ws = torch.empty(moe.grouped_mm_workspace_bytes(E), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(moe.grouped_mm_backward_workspace_bytes(M, K, E, N), dtype=torch.uint8, device="cuda")
     y = moe.grouped_mm(xd, wd, o, out=out, ws=ws)
     assert moe.status_read(ws) == moe.OK
     assert y.data_ptr() == out.data_ptr()
@@ -164,7 +167,7 @@ def test_no_rows():
 def test_bad_offsets_are_reported_and_touch_nothing(off):
     x, w = torch.ones((8, 64), device="cuda").bfloat16(), torch.ones((3, 64, 64), device="cuda").bfloat16()
     out = torch.full((8, 64), 3.0, device="cuda").bfloat16()
-    ws = torch.empty(moe.grouped_mm_workspace_bytes(3), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(moe.grouped_mm_backward_workspace_bytes(8, 64, 3, 64), dtype=torch.uint8, device="cuda")
     y = moe.grouped_mm(x, w, dev_offsets(off), out=out, ws=ws)
     assert moe.status_read(ws) == moe.ERR_ARG and moe.last_device_status() == moe.ERR_ARG
     assert (y == 3).all()
@@ -190,6 +193,11 @@ LINEAR = [
     (256, 256, 256, "relu", True, True, True),
     (300, 1000, 136, "silu", True, True, True),
     (1030, 72, 520, "gelu", True, True, True),
+    # long reductions, few tiles: in parts forward, in dx, in dw
+    (290, 16008, 520, "gelu", True, True, True),
+    (257, 16000, 264, "none", False, False, False),
+    (520, 40, 16008, "silu", False, False, False),
+    (2500, 264, 264, "relu", True, False, True),
 ]
 
 
@@ -335,7 +343,7 @@ def test_many_experts():
     off = offsets_of(counts)
     x, dy = rand(gen, off[-1], K), rand(gen, off[-1], N)
     w = rand(gen, E, N, K, scale=K ** -0.5)
-    ws = torch.full((moe.grouped_mm_workspace_bytes(E),), 255, dtype=torch.uint8, device="cuda")
+    ws = torch.full((moe.grouped_mm_backward_workspace_bytes(off[-1], K, E, N),), 255, dtype=torch.uint8, device="cuda")
     args = (x.cuda(), w.cuda(), dev_offsets(off))
     y = moe.grouped_mm(*args, ws=ws)
     assert moe.status_read(ws) == moe.OK
@@ -358,12 +366,48 @@ def test_workspace_contents_do_not_matter():
     got = []
     for fill in (0, 255):
         ws = lambda n: torch.full((n,), fill, dtype=torch.uint8, device="cuda")  # noqa: E731
-        a, b = ws(moe.grouped_mm_workspace_bytes(4)), ws(moe.linear_backward_workspace_bytes(133, 128, 264))
+        a, b = ws(moe.grouped_mm_backward_workspace_bytes(133, 128, 4, 264)), ws(moe.linear_backward_workspace_bytes(133, 128, 264))
         got.append((moe.grouped_mm(x, w, o, ws=a), *moe.grouped_mm_backward(dy, x, w, o, ws=a),
                     moe.linear(x, w[0], ws=ws(moe.linear_workspace_bytes(133, 128, 264))),
                     *moe.linear_backward(dy, x, w[0], z=dy, act="relu", bias=True, ws=b)))
         assert moe.status_read(a) == moe.OK and moe.status_read(b) == moe.OK
     assert all(torch.equal(p, q) for p, q in zip(*got))
+
+
+def test_parts_are_joined_in_order():
+    """Products whose reduction is shared by several pairs: one launch more, the same bits every time and
+    from a captured graph, whatever the workspace held; bad offsets leave zeros in dw."""
+    gen = torch.Generator().manual_seed(23)
+    x, w, res = rand(gen, 290, 16008).cuda(), rand(gen, 520, 16008, scale=0.01).cuda(), rand(gen, 290, 520).cuda()
+    a, b, v = rand(gen, 4000, 264).cuda(), rand(gen, 4000, 136).cuda(), rand(gen, 2, 136, 264).cuda()
+    o = dev_offsets([0, 3000, 4000])
+    n1, n2 = moe.linear_workspace_bytes(290, 16008, 520), moe.linear_backward_workspace_bytes(4000, 264, 136)
+    n3 = moe.grouped_mm_backward_workspace_bytes(4000, 264, 2, 136)
+
+    def run(fill):
+        ws = [torch.full((n,), fill, dtype=torch.uint8, device="cuda") for n in (n1, n2, n3)]
+        y = moe.linear(x, w, residual=res, act="silu", ws=ws[0])
+        launches = [moe.last_launch_count()]
+        dx, dw, _ = moe.linear_backward(b, a, v[0], ws=ws[1])
+        launches.append(moe.last_launch_count())
+        dx2, dw2 = moe.grouped_mm_backward(b, a, v, o, ws=ws[2], dw_dtype=torch.float32)
+        launches.append(moe.last_launch_count())
+        return [y, dx, dw, dx2, dw2], launches, ws
+
+    first, launches, _ = run(0)
+    assert launches == [3, 4, 4]
+    second = run(255)[0]
+    assert all(torch.equal(p, q) for p, q in zip(first, second))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        third, _, ws = run(255)
+    for t in third:
+        t.fill_(float("nan"))
+    graph.replay()
+    assert all(torch.equal(p, q) for p, q in zip(first, third))
+    ws = torch.full((n3,), 255, dtype=torch.uint8, device="cuda")
+    dw = moe.grouped_mm_backward(b, a, v, dev_offsets([0, 4000, 3000]), ws=ws, need_dx=False)[1]
+    assert moe.status_read(ws) == moe.ERR_ARG and (dw == 0).all()
 
 
 def test_another_stream_and_graph_replay():
