@@ -1102,30 +1102,42 @@ cudaError_t launch_rows(const void* a, const void* b, const MmArgs& m, cudaStrea
   }
 }
 
-// Four neighbouring values a thread: the parts' sums in their order, then the product's epilogue.  At
-// most 74 tiles' parts, which are in L2: its time is its latency.
-constexpr int kJoinThreads = 256;
-__global__ void __launch_bounds__(kJoinThreads) mm_join_kernel(const __grid_constant__ MmArgs p, int n4) {
+// Four neighbouring values a lane, one eighth of their parts a warp: each warp's sum in the parts' order, the
+// warps' sums in theirs (an order that the shape fixes), then the product's epilogue.  At most 74 tiles'
+// parts, which are in L2: its time is its latency, which one thread per value makes long.
+constexpr int kJoinWarps = 8;
+__global__ void __launch_bounds__(32 * kJoinWarps) mm_join_kernel(const __grid_constant__ MmArgs p, int n4) {
+  __shared__ float4 sums[kJoinWarps][32];
   pdl_wait();
   pdl_trigger();
-  const int at = blockIdx.x * kJoinThreads + threadIdx.x;
-  if (at >= n4) return;
-  const int col = at % (p.J / 4) * 4;
-  const float4* from = reinterpret_cast<const float4*>(p.parts) + at;
-  uint2 res = make_uint2(0, 0);
-  if (p.residual != nullptr) res = static_cast<const uint2*>(p.residual)[at];
-  const float4 bias = p.bias != nullptr ? __ldg(reinterpret_cast<const float4*>(p.bias + col))
-                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int at = blockIdx.x * 32 + lane;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int i = 0; i < p.split; ++i) {
-    const float4 o = __ldcg(from + (int64_t)i * n4);
+  if (at < n4) {
+    const float4* from = reinterpret_cast<const float4*>(p.parts) + at;
+    const int last = p.split * (warp + 1) / kJoinWarps;
+#pragma unroll 4
+    for (int i = p.split * warp / kJoinWarps; i < last; ++i) {
+      const float4 o = __ldcg(from + (int64_t)i * n4);
+      v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+    }
+  }
+  sums[warp][lane] = v;
+  __syncthreads();
+  if (warp != 0 || at >= n4) return;
+  for (int i = 1; i < kJoinWarps; ++i) {
+    const float4 o = sums[i][lane];
     v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
   }
   if (p.out_f32) {
     static_cast<float4*>(p.out)[at] = v;
     return;
   }
+  const int col = at % (p.J / 4) * 4;
+  uint2 res = make_uint2(0, 0);
+  if (p.residual != nullptr) res = static_cast<const uint2*>(p.residual)[at];
+  const float4 bias = p.bias != nullptr ? __ldg(reinterpret_cast<const float4*>(p.bias + col))
+                                        : make_float4(0.f, 0.f, 0.f, 0.f);
   with_act(p.act, p.fp16 != 0, [&](auto act, auto fp16) {
     store4<decltype(act)::value, decltype(fp16)::value>(p, v, bias, res, (int64_t)at * 4);
   });
@@ -1234,8 +1246,7 @@ cudaError_t launch_mm(int mode, const void* a, const void* b, const MmArgs& m, c
 
 cudaError_t launch_mm_join(int mode, const MmArgs& m, cudaStream_t stream) {
   const int64_t n4 = (mode == kMmWgrad ? (int64_t)m.E * m.I : m.rows) * m.J / 4;
-  return launch_pdl(mm_join_kernel, dim3((unsigned)((n4 + kJoinThreads - 1) / kJoinThreads)), dim3(kJoinThreads), 0,
-                    stream, m, (int)n4);
+  return launch_pdl(mm_join_kernel, dim3((unsigned)((n4 + 31) / 32)), dim3(32 * kJoinWarps), 0, stream, m, (int)n4);
 }
 
 }  // namespace nvfp4moe
