@@ -465,36 +465,29 @@ __global__ void __launch_bounds__(kG * kGroups, 1) norm_backward_kernel(const __
     turn ^= 1;
   }
   if (a.partials == nullptr) return;
-  float* part = a.partials + (int64_t)blockIdx.x * 2 * a.cols;
-  if constexpr (kGroups == 1) {
-#pragma unroll
-    for (int k = 0; k < kVecs; ++k)
-#pragma unroll
-      for (int i = 0; i < kVec; ++i)
-        if (c.has(k, i)) {
-          part[c.col(k) + i] = dg[k][i];
-          part[a.cols + c.col(k) + i] = db[k][i];
-        }
-    return;
-  }
-  // the groups' sums side by side in shared memory that is no longer used, added in group order
+  // The groups' sums side by side in shared memory that is no longer used, by place in the vectors (column
+  // + lead, which all rows of a CTA share), added in group order.  From there whole lines leave: stored
+  // by the threads that hold them, 8 columns apart, 21 rows x 12146 took 21.8 us.
   cp_async_wait<0>();
   __syncthreads();
-  float* s_sum = reinterpret_cast<float*>(s_dyn);      // [kGroups][2][cols]
-  static_assert(R::kBytes >= (size_t)kGroups * 2 * kG * kPer * sizeof(float), "the column sums fit the rings");
-  float* mine = s_sum + (size_t)group * 2 * a.cols;
+  constexpr int kPlaces = kG * kPer;
+  float* s_sum = reinterpret_cast<float*>(s_dyn);      // [kGroups][2][kPlaces]
+  static_assert(R::kBytes >= (size_t)kGroups * 2 * kPlaces * sizeof(float), "the column sums fit the rings");
+  float* mine = s_sum + (size_t)group * 2 * kPlaces;
 #pragma unroll
   for (int k = 0; k < kVecs; ++k)
 #pragma unroll
-    for (int i = 0; i < kVec; ++i)
-      if (c.has(k, i)) {
-        mine[c.col(k) + i] = dg[k][i];
-        mine[a.cols + c.col(k) + i] = db[k][i];
-      }
+    for (int i = 0; i < kVec; i += 4) {
+      float* to = mine + (k * kG + threadIdx.x % kG) * kVec + i;
+      *reinterpret_cast<float4*>(to) = make_float4(dg[k][i], dg[k][i + 1], dg[k][i + 2], dg[k][i + 3]);
+      *reinterpret_cast<float4*>(to + kPlaces) = make_float4(db[k][i], db[k][i + 1], db[k][i + 2], db[k][i + 3]);
+    }
   __syncthreads();
+  float* part = a.partials + (int64_t)blockIdx.x * 2 * a.cols;
   for (int i = threadIdx.x; i < 2 * a.cols; i += kThreads) {
-    float sum = s_sum[i];
-    for (int g = 1; g < kGroups; ++g) sum += s_sum[(size_t)g * 2 * a.cols + i];
+    const float* from = s_sum + (i < a.cols ? i : i - a.cols + kPlaces) + c.lead;
+    float sum = *from;
+    for (int g = 1; g < kGroups; ++g) sum += from[(size_t)g * 2 * kPlaces];
     part[i] = sum;
   }
 }
