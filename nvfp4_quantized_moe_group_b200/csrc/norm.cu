@@ -563,19 +563,15 @@ __global__ void __launch_bounds__(1024) norm_backward_wide_kernel(const __grid_c
     }
   }
   if (a.partials == nullptr) return;
+  __syncthreads();
+  // in whole lines: a column's place in the vectors is its own + lead, which all rows of a CTA share
+  const float* sums = reinterpret_cast<const float*>(s_acc);
   float* part = a.partials + (int64_t)blockIdx.x * 2 * a.cols;
-  for (int k = 0; c.some(k); ++k)
-#pragma unroll
-    for (int q = 0; q < kQuads; ++q) {
-      const float4 vg = s_acc[q * n_vecs + k * 1024 + threadIdx.x];
-      const float4 vb = s_acc[(kQuads + q) * n_vecs + k * 1024 + threadIdx.x];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (c.has(k, 4 * q + i)) {
-          part[c.col(k) + 4 * q + i] = (&vg.x)[i];
-          part[a.cols + c.col(k) + 4 * q + i] = (&vb.x)[i];
-        }
-    }
+  for (int i = threadIdx.x; i < 2 * a.cols; i += 1024) {
+    const int which = i >= a.cols, place = i - which * a.cols + c.lead;
+    const int quad = which * kQuads + place % kVec / 4;
+    part[i] = sums[(quad * n_vecs + place / kVec) * 4 + place % 4];
+  }
 }
 
 // Adds the CTAs' partial sums: 32 columns a CTA, 8 slices of the parts side by side.
