@@ -295,6 +295,48 @@ __device__ __forceinline__ void store_piece(const void* tmap, uint8_t* pieces, i
   }
 }
 
+// Forward, dgrad: features f0 on of a tile, one per lane of the warp's quarter of the accumulator, the token columns
+// first, first + step, ... 32 at a time.
+__device__ __forceinline__ void store_tokens(const MmArgs& p, const void* map_y, const void* map_z, uint32_t acc,
+                                             const Tile& t, int f0, int first, int step, int most, uint8_t* pieces,
+                                             int& turn, int lane) {
+  const bool col_ok = f0 + (lane & 3) * 8 < p.J;      // J is a multiple of 8
+  float bias[4];
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const int f = f0 + 8 * b + (lane >> 2);
+    bias[b] = p.bias != nullptr && f < p.J ? __ldg(p.bias + f) : 0.0f;
+  }
+  // the next piece's accumulator values and residual are on their way while one is stored; one copy of
+  // the code for all pieces, since straight-line code for all four ran at the rate of the instruction fetches
+  uint32_t v[2][16];
+  uint4 res[4];
+  auto fetch = [&](int c) {
+    if (c >= most || c >= t.rows_valid) return;
+    tmem_ld_16x256b_x4(acc + c, v[0]);
+    tmem_ld_16x256b_x4(acc + (16u << 16) + c, v[1]);
+    if (p.residual != nullptr) {
+      const uint16_t* from = static_cast<const uint16_t*>(p.residual) + f0 + (lane & 3) * 8;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = c + i * 8 + (lane >> 2);
+        res[i] = col_ok && r < t.rows_valid ? *reinterpret_cast<const uint4*>(from + (t.out_row + r) * (int64_t)p.J)
+                                            : make_uint4(0, 0, 0, 0);
+      }
+    }
+  };
+  fetch(first);
+  with_act(p.act, p.fp16 != 0, [&](auto act, auto fp16) {
+#pragma unroll 1
+    for (int c = first; c < t.rows_valid; c += step) {
+      tmem_ld_wait();
+      const PieceAt to{map_y, map_z, t.out_row + c, f0, t.rows_valid - c};
+      store_piece32<decltype(act)::value, decltype(fp16)::value>(p, to, pieces, turn, v, bias, res, lane,
+                                                                 [&] { fetch(c + step); });
+    }
+  });
+}
+
 // Tiles are handed out from a counter of the grid (the first is the pair's own index): tiles differ
 // in cost, so a fixed assignment left pairs idle (64 experts of skewed sizes, 32768 rows: 803 us).
 constexpr int kWorkRing = 4;             // tiles the loads may run ahead of the epilogue
@@ -563,44 +605,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
               if (f < p.J && c + i < t.rows_valid) to[(int64_t)i * p.J] = __uint_as_float(v[i]);
           }
         } else if (t.b0 + lane0 < p.J) {
-          const int f0 = t.b0 + lane0;
-          const bool col_ok = f0 + (lane & 3) * 8 < p.J;      // J is a multiple of 8
-          float bias[4];
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const int f = f0 + 8 * b + (lane >> 2);
-            bias[b] = p.bias != nullptr && f < p.J ? __ldg(p.bias + f) : 0.0f;
-          }
-          // the next piece's accumulator values and residual are on their way while one is stored; one
-          // copy of the code for all pieces, since straight-line code for all four ran at the rate of the
-          // instruction fetches
-          uint32_t v[2][16];
-          uint4 res[4];
-          auto fetch = [&](int c) {
-            if (c >= kPairTile || c >= t.rows_valid) return;
-            tmem_ld_16x256b_x4(acc + c, v[0]);
-            tmem_ld_16x256b_x4(acc + (16u << 16) + c, v[1]);
-            if (p.residual != nullptr) {
-              const uint16_t* from = static_cast<const uint16_t*>(p.residual) + f0 + (lane & 3) * 8;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int r = c + i * 8 + (lane >> 2);
-                res[i] = col_ok && r < t.rows_valid
-                             ? *reinterpret_cast<const uint4*>(from + (t.out_row + r) * (int64_t)p.J)
-                             : make_uint4(0, 0, 0, 0);
-              }
-            }
-          };
-          fetch(32 * part);
-          with_act(p.act, p.fp16 != 0, [&](auto act, auto fp16) {
-#pragma unroll 1
-            for (int c = 32 * part; c < t.rows_valid; c += 64) {
-              tmem_ld_wait();
-              const PieceAt to{&map_out, &map_z, t.out_row + c, f0, t.rows_valid - c};
-              store_piece32<decltype(act)::value, decltype(fp16)::value>(p, to, pieces, turn, v, bias, res, lane,
-                                                                         [&] { fetch(c + 64); });
-            }
-          });
+          store_tokens(p, &map_out, &map_z, acc, t, t.b0 + lane0, 32 * part, 64, kPairTile, pieces, turn, lane);
         }
       } else {
         // this warp's 64-column pieces, all in registers before any is stored, so that the accumulator is
@@ -681,15 +686,17 @@ __host__ __device__ constexpr int clusters_that_fit(int split) {
 template <int kTok>
 struct NarrowCfg {
   static constexpr int kStages = kTok <= 16 ? 10 : kTok <= 32 ? 9 : kTok <= 64 ? 7 : 5;
-  static constexpr uint32_t kAccCols = kTok < 16 ? 16 : kTok;
-  static constexpr uint32_t kTmemCols = 2 * kAccCols < 32 ? 32 : 2 * kAccCols;
+  static constexpr uint32_t kAccCols = kTok < 32 ? 32 : kTok;      // the epilogue reads 32 at a time
+  static constexpr uint32_t kTmemCols = 2 * kAccCols;
+  static constexpr int kPartRows = kTok < 64 ? 64 : kTok;
 };
 
 template <int kTok>
 struct __align__(1024) NarrowSmem {
   uint8_t w[NarrowCfg<kTok>::kStages][kOperandBytes];
   uint8_t x[NarrowCfg<kTok>::kStages][kTok * kBK * 2];
-  float part[kTok][kHalf];            // this CTA's sums of the tile, token-major
+  // split > 1: this CTA's sums of the tile, token-major; else four token pieces a warp
+  float part[NarrowCfg<kTok>::kPartRows][kHalf];
   uint64_t full[NarrowCfg<kTok>::kStages];
   uint64_t empty[NarrowCfg<kTok>::kStages];
   uint64_t acc_full[2];
@@ -731,6 +738,7 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
 template <int kMode, int kTok>
 __global__ void __launch_bounds__(kNarrowThreads, 1)
 mm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                 const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_z,
                  const __grid_constant__ MmArgs p, int split) {
   using C = NarrowCfg<kTok>;
   constexpr int kStages = C::kStages;
@@ -859,9 +867,26 @@ mm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
   } else if (warp >= 4) {
     // ----------------------------------------------------------- epilogue ----
     const int q = warp & 3;
-    int it = 0;
+    static_assert(sizeof(s.part) >= 16 * kTokenPiece, "the epilogue's pieces");
+    uint8_t* pieces = reinterpret_cast<uint8_t*>(s.part) + q * 4 * kTokenPiece;
+    int it = 0, turn = 0;
     for (int w = first; w < total; w += step, ++it) {
       const Tile t = tile_at<kMode>(p, w, kTok, kHalf);
+      if (split == 1) {                      // each warp by itself
+        const bool got = wait_cluster(&s.acc_full[it & 1], (uint32_t)(it >> 1) & 1u, &s.abort_flag);
+        if (__any_sync(0xffffffffu, !got)) {
+          set_abort(&s.abort_flag, p.status);
+          break;
+        }
+        tc_fence_after();
+        if (t.b0 + q * 32 < p.J)
+          store_tokens(p, &map_out, &map_z, tmem + (uint32_t)(it & 1) * C::kAccCols + ((uint32_t)(q * 32) << 16), t,
+                       t.b0 + q * 32, 0, 32, kTok, pieces, turn, lane);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.acc_empty[it & 1]);
+        continue;
+      }
       bool got = wait_cluster(&s.acc_full[it & 1], (uint32_t)(it >> 1) & 1u, &s.abort_flag);
       // the tile before this one has been read by every CTA of the cluster
       if (it > 0) got = got && wait_cluster(&s.part_empty, (uint32_t)(it - 1) & 1u, &s.abort_flag);
@@ -883,11 +908,7 @@ mm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.acc_empty[it & 1]);
-      if (split == 1) {
-        if (lane == 0) mbar_arrive(&s.part_full);
-      } else if (lane < split) {
-        mbar_arrive_rank_release(&s.part_full, lane);
-      }
+      if (lane < split) mbar_arrive_rank_release(&s.part_full, lane);
       const bool all = wait_cluster(&s.part_full, (uint32_t)it & 1u, &s.abort_flag);
       if (__any_sync(0xffffffffu, !all)) {
         set_abort(&s.abort_flag, p.status);
@@ -914,16 +935,11 @@ mm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
             for (int i = 0; i < 4; ++i) {
               const int r = r0 + 4 * split * i;
               if (r >= t.rows_valid) continue;
-              float4 v;
-              if (split == 1) {
-                v = *reinterpret_cast<const float4*>(&s.part[r][4 * lane]);
-              } else {
-                v = make_float4(0.f, 0.f, 0.f, 0.f);
-                const uint32_t at = smem_u32(&s.part[r][4 * lane]);
-                for (int c = 0; c < split; ++c) {
-                  const float4 o = ld_cluster_f4(map_rank(at, c));
-                  v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
-                }
+              float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+              const uint32_t at = smem_u32(&s.part[r][4 * lane]);
+              for (int c = 0; c < split; ++c) {
+                const float4 o = ld_cluster_f4(map_rank(at, c));
+                v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
               }
               store4<decltype(act)::value, decltype(fp16)::value>(p, v, bias, res[i], at0 + r * (int64_t)p.J);
             }
@@ -931,12 +947,9 @@ mm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
         });
       }
       __syncwarp();
-      if (split == 1) {
-        if (lane == 0) mbar_arrive(&s.part_empty);
-      } else if (lane < split) {
-        mbar_arrive_rank(&s.part_empty, lane);
-      }
+      if (lane < split) mbar_arrive_rank(&s.part_empty, lane);
     }
+    if (lane == 0) bulk_wait_all0();
   }
 
   __syncwarp();
@@ -1061,9 +1074,14 @@ cudaError_t launch_pair(const void* a, const void* b, const MmArgs& args, cudaSt
 template <int kMode, int kTok>
 cudaError_t launch_narrow(const void* a, const void* b, const MmArgs& m, int split, cudaStream_t stream) {
   CUtensorMap map_w, map_x;
-  const int err = (kMode == kMmForward ? make_tma_16(&map_w, b, m.R, m.J, m.E, kHalf)
-                                       : make_tma_16(&map_w, b, m.J, m.R, m.E, kBK)) |
-                  make_tma_16(&map_x, a, m.R, m.rows, 1, kTok);
+  int err = (kMode == kMmForward ? make_tma_16(&map_w, b, m.R, m.J, m.E, kHalf)
+                                 : make_tma_16(&map_w, b, m.J, m.R, m.E, kBK)) |
+            make_tma_16(&map_x, a, m.R, m.rows, 1, kTok);
+  CUtensorMap map_out = map_x, map_z = map_x;          // used for whole pieces of tiles that are not shared
+  if (split == 1 && kTok >= 32) {
+    err |= make_tma_3d(&map_out, m.out, 2, m.J, m.rows, 1, 32, 64);
+    if (m.z_out != nullptr) err |= make_tma_3d(&map_z, m.z_out, 2, m.J, m.rows, 1, 32, 64);
+  }
   if (err != 0) return cudaErrorInvalidValue;
   const size_t smem = sizeof(NarrowSmem<kTok>) + 1024;
   static_assert(sizeof(NarrowSmem<kTok>) + 1024 <= 232448, "shared memory exceeds the per-block limit");
@@ -1088,7 +1106,7 @@ cudaError_t launch_narrow(const void* a, const void* b, const MmArgs& m, int spl
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = split > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, map_w, map_x, m, split);
+  return cudaLaunchKernelEx(&cfg, kernel, map_w, map_x, map_out, map_z, m, split);
 }
 
 template <int kMode>
@@ -1146,15 +1164,17 @@ __global__ void __launch_bounds__(32 * kJoinWarps) mm_join_kernel(const __grid_c
 // Where pairs share reductions: at most this many tiles of parts, one for each pair.
 constexpr int kPairs = 74;
 // SM clocks of the launch that joins `split` parts of n values, and of writing them.
-double join_cost(int split, double n) { return 5000.0 + split * n * 8.0 / 2500.0; }
+double join_cost(int split, double n) { return 5000.0 + split * n * 8.0 / 2000.0; }
 
 }  // namespace
 
 // The cheapest of the shapes by a model in SM clocks.  A tile's step takes the time to bring its
-// operands in (about 45 bytes a clock and SM, latency included) or the tensor time; waves of tiles follow one
-// another; and nothing is faster than the weights from HBM (3500 bytes a clock).  Measured at K = N =
-// 5120: 16 rows 11.0 us on single CTAs split 3 ways, 18.6 on pairs; 128 rows 17.1 and 20.5; 384 rows
-// 27.4 and 24.5; 16 experts of 96 rows 93.3 and 90.4, of 192 rows 122 and 100.
+// operands in: about 45 bytes a clock and SM, 72 on single CTAs whose weights other row tiles read too (from
+// L2; 48 where rows are not whole lines), but then 360 clocks at least.  Waves of tiles follow one another, each as long as its steps or
+// the epilogue of the one before; the weights from HBM (3500 bytes a clock) run beside all that.  Measured, us,
+// single CTAs (the best of them) and pairs: K = N = 5120: 16 rows 11.3 (split 3 ways) and 19.7, 256 rows 20.7 and
+// 22.7, 768 rows 39 and 34; K = N = 2560: 512 rows 13.3 and 14.4; K = 64, 8192 x 8192: 69 and 44; 16 experts of
+// 192 rows, K = 5120, N = 2560: 118 and 99.  Over 30 shapes the choice was 2 % slower than the best one.
 MmPlan mm_plan(int64_t rows, int E, int J, int R, bool ragged) {
   const int64_t steps = (R + kBK - 1) / kBK;
   // how the rows spread over the experts is known on the device only: evenly, for the model
@@ -1163,6 +1183,7 @@ MmPlan mm_plan(int64_t rows, int E, int J, int R, bool ragged) {
   MmPlan best{false, 16, 1};
   if (mean == 0) return best;
   const double hbm = (double)busy * J * R * 2.0 / 3500.0;
+  const bool whole_lines = R % 64 == 0 && J % 64 == 0;       // the copies' 128-byte rows are lines of the L2
   double best_cost = 1e30;
   auto consider = [&](bool pair, int tile, int split) {
     const int64_t per_seg = (mean + tile - 1) / tile, cols = pair ? kPairTile : kHalf;
@@ -1171,14 +1192,16 @@ MmPlan mm_plan(int64_t rows, int E, int J, int R, bool ragged) {
     const int64_t room = pair ? kPairs : clusters_that_fit(split);
     const int64_t waves = pair && split > 1 ? 1 : (tiles + room - 1) / room;
     const double n = pair ? (double)(((mean + per_seg - 1) / per_seg + 31) / 32 * 32) : (double)tile;
-    double step = (16384.0 + (pair ? 64.0 : 128.0) * n) / 45.0;
-    if (step < 2.0 * n) step = 2.0 * n;
+    const bool from_l2 = !pair && split == 1 && per_seg > 1;   // mostly, the weights that another row tile reads too
+    double step = (16384.0 + (pair ? 64.0 : 128.0) * n) / (!from_l2 ? 45.0 : whole_lines ? 72.0 : 48.0);
+    if (from_l2 && step < 360.0) step = 360.0;
     const double mma = (double)((steps + split - 1) / split) * step;
-    const double epilogue = pair ? 2300.0 + 14.0 * n : 1900.0 + 68.0 * n;
+    const double epilogue = pair ? 2300.0 + 14.0 * n : split == 1 ? 2000.0 + 20.0 * n : 2500.0 + 76.0 * n;
     double cost = mma + (double)(waves - 1) * (mma > epilogue ? mma : epilogue);
-    if (cost < hbm) cost = hbm;
-    cost += pair ? 4000.0 + 12.0 * n + (split > 1 ? join_cost(split, (double)rows * J) : 0.0)
-                 : 2500.0 + 25.0 * n + (split > 1 ? (600.0 + 8.0 * n) * (double)waves : 0.0);
+    cost = cost < hbm ? hbm + 0.2 * cost : cost + 0.2 * hbm;   // the two overlap, but not wholly
+    cost += pair         ? 6000.0 + 6.0 * n + (split > 1 ? join_cost(split, (double)rows * J) : 0.0)
+            : split == 1 ? 2500.0 + 5.0 * n
+                         : 2500.0 + 25.0 * n + (600.0 + 8.0 * n) * (double)waves;
     if (cost < best_cost) {
       best_cost = cost;
       best = MmPlan{pair, tile, split};

@@ -195,6 +195,7 @@ LINEAR = [
     (1030, 72, 520, "gelu", True, True, True),
     # long reductions, few tiles: in parts forward, in dx, in dw
     (290, 16008, 520, "gelu", True, True, True),
+    (600, 16008, 264, "gelu", True, True, True),
     (257, 16000, 264, "none", False, False, False),
     (520, 40, 16008, "silu", False, False, False),
     (2500, 264, 264, "relu", True, False, True),
@@ -378,10 +379,10 @@ def test_parts_are_joined_in_order():
     """Products whose reduction is shared by several pairs: one launch more, the same bits every time and
     from a captured graph, whatever the workspace held; bad offsets leave zeros in dw."""
     gen = torch.Generator().manual_seed(23)
-    x, w, res = rand(gen, 290, 16008).cuda(), rand(gen, 520, 16008, scale=0.01).cuda(), rand(gen, 290, 520).cuda()
+    x, w, res = rand(gen, 600, 16008).cuda(), rand(gen, 264, 16008, scale=0.01).cuda(), rand(gen, 600, 264).cuda()
     a, b, v = rand(gen, 4000, 264).cuda(), rand(gen, 4000, 136).cuda(), rand(gen, 2, 136, 264).cuda()
     o = dev_offsets([0, 3000, 4000])
-    n1, n2 = moe.linear_workspace_bytes(290, 16008, 520), moe.linear_backward_workspace_bytes(4000, 264, 136)
+    n1, n2 = moe.linear_workspace_bytes(600, 16008, 264), moe.linear_backward_workspace_bytes(4000, 264, 136)
     n3 = moe.grouped_mm_backward_workspace_bytes(4000, 264, 2, 136)
 
     def run(fill):
