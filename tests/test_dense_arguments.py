@@ -118,6 +118,22 @@ def test_product_types_and_pointers(lib):
     assert linear_backward(lib, db=A + 2) == moe.ERR_ARG
 
 
+def test_parts_need_their_workspace(lib):
+    """Calls whose reduction is shared by several pairs refuse the workspace of those without."""
+    need = moe.grouped_mm_backward_workspace_bytes(1 << 20, 64, 1, 128)
+    kw = dict(M=1 << 20, K=64, E=1, N=128)
+    assert grouped_backward(lib, ws_bytes=need - 1, **kw) == moe.ERR_WORKSPACE
+    assert grouped_backward(lib, ws_bytes=need, **kw) in NO_DEVICE
+    kw = dict(M=600, K=16008, N=264)
+    need = moe.linear_workspace_bytes(600, 16008, 264)
+    assert need > 9 * 4 * 600 * 264
+    assert linear(lib, ws_bytes=need - 1, **kw) == moe.ERR_WORKSPACE and linear(lib, ws_bytes=need, **kw) in NO_DEVICE
+    kw = dict(M=520, K=40, N=16008)
+    need = moe.linear_backward_workspace_bytes(520, 40, 16008)
+    assert linear_backward(lib, ws_bytes=need - 1, **kw) == moe.ERR_WORKSPACE
+    assert linear_backward(lib, ws_bytes=need, **kw) in NO_DEVICE
+
+
 def test_no_rows_need_no_row_pointers(lib):
     assert grouped(lib, M=0, x=None, y=None) in NO_DEVICE
     assert linear(lib, M=0, x=None, y=None) in NO_DEVICE
