@@ -146,7 +146,6 @@ __device__ __forceinline__ void store_piece32(const MmArgs& p, const PieceAt& to
     if (lane == 0) {
       if (p.z_out != nullptr) tma_store_3d(to.map_z, p_z, to.f0, (int)to.row, 0);
       tma_store_3d(to.map_y, p_y, to.f0, (int)to.row, 0);
-      bulk_commit();
     }
   } else {                                       // a segment's last rows: the rows behind are not this tile's
     __syncwarp();
@@ -156,6 +155,9 @@ __device__ __forceinline__ void store_piece32(const MmArgs& p, const PieceAt& to
       rows_to_global(static_cast<uint16_t*>(p.out), p_y, at, p.J, to.live, lane);
     }
   }
+  // One group a piece, an empty one for rows stored by the lanes: the wait above leaves the newest group
+  // pending, which then is never that of the piece about to be written.
+  if (lane == 0) bulk_commit();
 }
 
 }  // namespace nvfp4moe
