@@ -295,7 +295,9 @@ cudaError_t launch_repack_sf(const uint8_t* linear, int rows, int cols16, uint8_
 int num_sms();
 
 // Allows `kernel` this much dynamic shared memory on the current device; remembers, per host thread,
-// what it has already set (the runtime call costs a good part of a small kernel's launch).
+// what it has already set (the runtime call costs a good part of a small kernel's launch).  The limit belongs to
+// the kernel on the device, for all threads: every call for a kernel passes the same `bytes`, the most that any of
+// its launches takes, or one thread's call would lower what another remembers as set.
 cudaError_t allow_smem(const void* kernel, size_t bytes);
 
 // Zeroes the first `words` 32-bit words of a call's status header on the stream and records

@@ -709,7 +709,10 @@ cudaError_t backward_wide(const NormArgs& a, int ctas, cudaStream_t stream) {
   const int n_vecs = (span_of(a.cols, vec_of(kType)) + vec_of(kType) - 1) / vec_of(kType);
   const size_t smem = (size_t)n_vecs * vec_of(kType) * 2 * sizeof(float);
   const auto kernel = norm_backward_wide_kernel<kType, kAligned>;
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), smem);
+  // the limit for the widest row, whatever this call's: see allow_smem
+  constexpr size_t kWidest = (size_t)(kNormMaxCols + 8) * 2 * sizeof(float);
+  static_assert(kWidest + 1024 <= 232448, "shared memory exceeds the per-block limit");
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), kWidest);
   if (e != cudaSuccess) return e;
   return launch_pdl(kernel, dim3(ctas), dim3(1024), smem, stream, a, n_vecs);
 }
