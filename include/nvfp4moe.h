@@ -619,6 +619,14 @@ NVFP4MOE_API int nvfp4moe_linear_backward(int32_t dtype, const void* dy, const v
                                           int64_t M, int32_t K, int32_t N, int32_t act, void* dx, void* dw,
                                           int32_t dw_dtype, float* db, void* ws, size_t ws_bytes, void* stream);
 
+/* Debugging aids of the product calls that this host thread makes from here on (both 0 at first):
+ *   wait_limit_us      limit of each bounded wait inside their kernels in microseconds; 0: 1.5 s, below
+ *                      1000 counts as 1000
+ *   inject_skip_loads  test hook: n > 0 makes the n-th CTA of each product kernel bring in no operands, so that the
+ *                      waits for them run out and the call reports NVFP4MOE_ERR_TIMEOUT; its outputs are then
+ *                      unspecified; below 0 NVFP4MOE_ERR_ARG */
+NVFP4MOE_API int nvfp4moe_product_debug(uint32_t wait_limit_us, int32_t inject_skip_loads);
+
 /* Layer norm over the rows of x [rows][cols] (any cols from 1 to 28672, 0 <= rows < 2^31), type BF16,
  * FP16 or FP32, arithmetic and parameters FP32:
  *   y = (x - mean) rstd gamma + beta,   rstd = 1 / sqrt(mean_j((x - mean)^2) + eps)

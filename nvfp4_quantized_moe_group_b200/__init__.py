@@ -36,7 +36,7 @@ from ._lib import (  # noqa: F401
     ep_combine, forward_partial_peer, ipc_handle, ipc_open, ipc_close,
     grouped_mm, grouped_mm_backward, grouped_mm_workspace_bytes, grouped_mm_backward_workspace_bytes,
     linear, linear_backward, linear_workspace_bytes,
-    linear_backward_workspace_bytes, layer_norm, layer_norm_backward, layer_norm_backward_workspace_bytes,
+    linear_backward_workspace_bytes, product_debug, layer_norm, layer_norm_backward, layer_norm_backward_workspace_bytes,
     status_string, last_launch_count, forward_workspace_bytes, route_workspace_bytes,
     quantize_workspace_bytes, swizzled_scale_bytes, declared_symbols, lib, LIB_PATH, StageTimer, STAGES,
     OK, ERR_ARG, ERR_SHAPE, ERR_CUDA, ERR_WORKSPACE, ERR_NONFINITE, ERR_TIMEOUT, ERR_DEVICE,

@@ -153,6 +153,7 @@ _SIGS = {
     "nvfp4moe_linear_backward_workspace_bytes": (_SZ, [_I64, ctypes.c_int32, ctypes.c_int32]),
     "nvfp4moe_linear_backward": (ctypes.c_int, [ctypes.c_int32, _P, _P, _P, _P, _I64, ctypes.c_int32, ctypes.c_int32,
                                                 ctypes.c_int32, _P, _P, ctypes.c_int32, _P, _P, _SZ, _P]),
+    "nvfp4moe_product_debug": (ctypes.c_int, [ctypes.c_uint32, ctypes.c_int32]),
     "nvfp4moe_layer_norm": (ctypes.c_int, [ctypes.c_int32, _P, _I64, ctypes.c_int32, _P, _P, ctypes.c_float,
                                            ctypes.c_int32, _P, _P, _P, _P]),
     "nvfp4moe_layer_norm_backward_workspace_bytes": (_SZ, [_I64, ctypes.c_int32]),
@@ -978,6 +979,12 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, z: torch
            "nvfp4moe_linear_backward")
     _keep(stream, dx, dw, db, ws)
     return dx, dw, db
+
+
+def product_debug(wait_limit_us: int = 0, inject_skip_loads: int = 0):
+    """Wait limit of the product calls that this host thread makes from here on (0: 1.5 s), and the test hook
+    that makes their waits run out (nvfp4moe_product_debug); without arguments, back to the defaults."""
+    _check(lib().nvfp4moe_product_debug(int(wait_limit_us), int(inject_skip_loads)), "nvfp4moe_product_debug")
 
 
 def layer_norm(x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.Tensor | None = None,

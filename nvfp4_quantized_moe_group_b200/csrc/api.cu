@@ -398,6 +398,10 @@ bool product_shape(int64_t M, int32_t K, int32_t N, int32_t E) {
   return M * (int64_t)(K > N ? K : N) < kMaxElems && (int64_t)K * N < kMaxElems / E;
 }
 
+// Set by nvfp4moe_product_debug for the product calls of this host thread.
+thread_local uint64_t g_product_wait_ns = kWaitLimitNs;
+thread_local int32_t g_product_skip_loads = 0;
+
 struct ProductWs {
   WsHeader* hdr;
   int32_t* seg;
@@ -465,6 +469,8 @@ MmArgs product_args(const ProductWs& p, bool ragged, int E, int64_t M, int32_t d
   m.rows = M;
   m.fp16 = dtype == NVFP4MOE_FP16;
   m.status = &p.hdr->status;
+  m.wait_ns = g_product_wait_ns;
+  m.skip_loads = g_product_skip_loads;
   m.work_counter = ragged ? &p.hdr->work[0] : nullptr;
   return m;
 }
@@ -1707,6 +1713,13 @@ int nvfp4moe_ep_combine(const float* rows, const int32_t* send_pos, int64_t T, i
       cudaSuccess)
     return cuda_failed();
   g_launches = 1;
+  return NVFP4MOE_OK;
+}
+
+int nvfp4moe_product_debug(uint32_t wait_limit_us, int32_t inject_skip_loads) {
+  if (inject_skip_loads < 0) return NVFP4MOE_ERR_ARG;
+  g_product_wait_ns = wait_limit_us == 0 ? kWaitLimitNs : 1000ull * (wait_limit_us < 1000 ? 1000 : wait_limit_us);
+  g_product_skip_loads = inject_skip_loads;
   return NVFP4MOE_OK;
 }
 

@@ -32,8 +32,8 @@
 // the loads fill zeros behind its end.  (Zeroing those lines in shared memory before the MMAs
 // cost every tile a cross-CTA fence: 64 skewed experts, 32768 rows, 1011 us.)
 //
-// Every wait is bounded; one that runs out raises the timeout bit of the status word and the
-// pair winds down.
+// Every wait is bounded; one that runs out raises the timeout bit of the status word and the abort flag of
+// every CTA of its cluster, which wind down together.
 //
 // Measured: 4096 x 5120 x 5120 150 us (1.43 PFLOP/s), 4096 x 20480, K = 5120 with GELU and saved sums 587 us
 // (1.46 PFLOP/s); 64 skewed experts, 32768 rows, 2560 -> 5120 704 to 757 us; both gradients of 32 experts, 8192 rows,
@@ -97,13 +97,14 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t pa
 }
 
 // mbar_wait with cluster-scope acquire, ended early by the CTA's abort flag.
-__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, const int* abort_flag) {
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, const int* abort_flag,
+                                             uint64_t limit_ns) {
   if (mbar_try_wait_cluster(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   uint32_t n = 0;
   while (!mbar_try_wait_cluster(bar, parity)) {
     if ((++n & 63u) == 0u &&
-        (*reinterpret_cast<const volatile int*>(abort_flag) != 0 || globaltimer_ns() - t0 > kWaitLimitNs))
+        (*reinterpret_cast<const volatile int*>(abort_flag) != 0 || globaltimer_ns() - t0 > limit_ns))
       return false;
   }
   return true;
@@ -117,9 +118,13 @@ __device__ __forceinline__ void store_rank(int* dst, uint64_t* bar, uint32_t ran
                : "memory");
 }
 
-__device__ __forceinline__ void set_abort(int* flag, uint32_t* status) {
+// Reports a wait that ran out and ends those of every CTA of the cluster (each is there until the barrier at the
+// kernel's end, which this thread has still to pass).
+__device__ __forceinline__ void set_abort(int* flag, uint32_t* status, int ctas) {
   raise_status(status, kStatusTimeout);
-  *reinterpret_cast<volatile int*>(flag) = 1;
+  for (int r = 0; r < ctas; ++r)
+    asm volatile("st.relaxed.cluster.shared::cluster.b32 [%0], %1;" ::"r"(map_rank(smem_u32(flag), (uint32_t)r)), "r"(1)
+                 : "memory");
 }
 
 // Tiled load into this CTA's shared memory, completion counted on a barrier of either CTA of the
@@ -365,9 +370,9 @@ struct __align__(1024) PairSmem {
 // The next tile of a reader (a whole warp, or one thread): -1 when there are no more, -2 when the wait
 // ran out.  Frees the slot once every lane has read it.
 template <bool kWarp>
-__device__ __forceinline__ int next_tile(PairSmem& s, int it, int lane) {
+__device__ __forceinline__ int next_tile(PairSmem& s, int it, int lane, uint64_t limit_ns) {
   const int slot = it & (kWorkRing - 1);
-  bool got = wait_cluster(&s.work_full[slot], (uint32_t)(it / kWorkRing) & 1u, &s.abort_flag);
+  bool got = wait_cluster(&s.work_full[slot], (uint32_t)(it / kWorkRing) & 1u, &s.abort_flag, limit_ns);
   if (kWarp) got = __all_sync(0xffffffffu, got);
   if (!got) return -2;
   const int w = *reinterpret_cast<volatile int*>(&s.work[slot]);
@@ -437,8 +442,8 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         const int slot = it & (kWorkRing - 1);
         int w;
         if (rank == 0) {
-          if (!wait_cluster(&s.work_empty[slot], ((uint32_t)(it / kWorkRing) & 1u) ^ 1u, &s.abort_flag)) {
-            set_abort(&s.abort_flag, p.status);
+          if (!wait_cluster(&s.work_empty[slot], ((uint32_t)(it / kWorkRing) & 1u) ^ 1u, &s.abort_flag, p.wait_ns)) {
+            set_abort(&s.abort_flag, p.status, 2);
             ok = false;
             break;
           }
@@ -455,13 +460,17 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
           mbar_arrive(&s.work_full[slot]);
         } else {
           mbar_arrive_expect_tx(&s.work_full[slot], 4);
-          w = next_tile<false>(s, it, lane);
+          w = next_tile<false>(s, it, lane, p.wait_ns);
           if (w == -2) {
-            set_abort(&s.abort_flag, p.status);
+            set_abort(&s.abort_flag, p.status, 2);
             ok = false;
           }
         }
         if (w < 0) break;
+        if (p.skip_loads == (int)blockIdx.x + 1) {           // test hook: what these loads would bring never comes
+          ok = false;
+          break;
+        }
         const Tile t = tile_at<kMode>(p, w, tile_i, kPairTile);
         // wgrad: 128 rows of each operand; else 128 features, and half of the tile's token rows in
         // the smallest box that covers them
@@ -481,8 +490,8 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         }
         const uint32_t b_bytes = (half > 64 ? kHalf : half > 32 ? 64 : 32) * kBK * 2;
         for (int k = 0; k < t.steps; ++k) {
-          if (!wait_cluster(&s.empty[stage], phase ^ 1u, &s.abort_flag)) {
-            set_abort(&s.abort_flag, p.status);
+          if (!wait_cluster(&s.empty[stage], phase ^ 1u, &s.abort_flag, p.wait_ns)) {
+            set_abort(&s.abort_flag, p.status, 2);
             ok = false;
             break;
           }
@@ -509,8 +518,8 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
       // this CTA waits for the last of those arrivals: without this one could reach the shared memory
       // of a CTA that has exited, or of the next kernel's.  It also shows that every copy has landed.
       for (int i = 0; ok && i < kPairStages; ++i) {
-        if (!wait_cluster(&s.empty[stage], phase ^ 1u, &s.abort_flag)) {
-          set_abort(&s.abort_flag, p.status);
+        if (!wait_cluster(&s.empty[stage], phase ^ 1u, &s.abort_flag, p.wait_ns)) {
+          set_abort(&s.abort_flag, p.status, 2);
           ok = false;
         }
         if (++stage == kPairStages) { stage = 0; phase ^= 1u; }
@@ -529,9 +538,9 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
       bool ok = true;
       int it = 0;                            // tiles with an accumulator
       for (int n = 0; ok; ++n) {
-        const int w = next_tile<false>(s, n, lane);
+        const int w = next_tile<false>(s, n, lane, p.wait_ns);
         if (w < 0) {
-          if (w == -2) set_abort(&s.abort_flag, p.status);
+          if (w == -2) set_abort(&s.abort_flag, p.status, 2);
           break;
         }
         const Tile t = tile_at<kMode>(p, w, tile_i, kPairTile);
@@ -539,14 +548,14 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         const uint32_t idesc =
             idesc_f16(2 * kHalf, kTokens ? pair_columns(t.rows_valid) : kPairTile, p.fp16 != 0, kAMn, kBMn);
         const uint32_t acc = tmem + (uint32_t)(it & 1) * kPairTile;
-        if (!wait_cluster(&s.acc_empty[it & 1], ((uint32_t)(it >> 1) & 1u) ^ 1u, &s.abort_flag)) {
-          set_abort(&s.abort_flag, p.status);
+        if (!wait_cluster(&s.acc_empty[it & 1], ((uint32_t)(it >> 1) & 1u) ^ 1u, &s.abort_flag, p.wait_ns)) {
+          set_abort(&s.abort_flag, p.status, 2);
           break;
         }
         tc_fence_after();
         for (int k = 0; k < t.steps; ++k) {
-          if (!wait_cluster(&s.full[stage], phase, &s.abort_flag)) {
-            set_abort(&s.abort_flag, p.status);
+          if (!wait_cluster(&s.full[stage], phase, &s.abort_flag, p.wait_ns)) {
+            set_abort(&s.abort_flag, p.status, 2);
             ok = false;
             break;
           }
@@ -568,7 +577,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
       }
       // every tensor-core operation of the pair is done before the memories are given back
       tc_commit_pair_local(&s.drain);
-      if (!mbar_wait(&s.drain, 0)) set_abort(&s.abort_flag, p.status);
+      if (!mbar_wait(&s.drain, 0)) set_abort(&s.abort_flag, p.status, 2);
     }
   } else if (warp >= 4) {
     // ----------------------------------------------------------- epilogue ----
@@ -578,17 +587,17 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     int turn = 0;
     int it = 0;                              // tiles with an accumulator
     for (int n = 0;; ++n) {
-      const int w = next_tile<true>(s, n, lane);
+      const int w = next_tile<true>(s, n, lane, p.wait_ns);
       if (w < 0) {
-        if (w == -2) set_abort(&s.abort_flag, p.status);
+        if (w == -2) set_abort(&s.abort_flag, p.status, 2);
         break;
       }
       const Tile t = tile_at<kMode>(p, w, tile_i, kPairTile);
       const bool has_acc = t.steps > 0;
       if (has_acc) {
-        const bool got = wait_cluster(&s.acc_full[it & 1], (uint32_t)(it >> 1) & 1u, &s.abort_flag);
+        const bool got = wait_cluster(&s.acc_full[it & 1], (uint32_t)(it >> 1) & 1u, &s.abort_flag, p.wait_ns);
         if (__any_sync(0xffffffffu, !got)) {
-          set_abort(&s.abort_flag, p.status);
+          set_abort(&s.abort_flag, p.status, 2);
           break;
         }
         tc_fence_after();
@@ -798,10 +807,14 @@ mm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
       uint32_t stage = 0, phase = 0, issued = 0, issued_par = 0;
       bool ok = true;
       for (int w = first; ok && w < total; w += step) {
+        if (p.skip_loads == (int)blockIdx.x + 1) {           // test hook, as in the pairs
+          ok = false;
+          break;
+        }
         const Tile t = tile_at<kMode>(p, w, kTok, kHalf);
         for (int k = k0; k < k1; ++k) {
-          if (!wait_cluster(&s.empty[stage], phase ^ 1u, &s.abort_flag)) {
-            set_abort(&s.abort_flag, p.status);
+          if (!wait_cluster(&s.empty[stage], phase ^ 1u, &s.abort_flag, p.wait_ns)) {
+            set_abort(&s.abort_flag, p.status, split);
             ok = false;
             break;
           }
@@ -821,8 +834,8 @@ mm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
       }
       // the MMAs have read every stage: no copy and no arrival of theirs is under way at the exit
       for (int i = 0; ok && i < kStages; ++i) {
-        if (!wait_cluster(&s.empty[stage], phase ^ 1u, &s.abort_flag)) {
-          set_abort(&s.abort_flag, p.status);
+        if (!wait_cluster(&s.empty[stage], phase ^ 1u, &s.abort_flag, p.wait_ns)) {
+          set_abort(&s.abort_flag, p.status, split);
           ok = false;
         }
         if (++stage == kStages) { stage = 0; phase ^= 1u; }
@@ -830,7 +843,7 @@ mm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
       // after giving up, the copies at least have landed
       for (int i = 0; !ok && i < kStages; ++i)
         if ((issued >> i) & 1u)
-          if (!mbar_wait(&s.full[i], (issued_par >> i) & 1u)) set_abort(&s.abort_flag, p.status);
+          if (!mbar_wait(&s.full[i], (issued_par >> i) & 1u)) set_abort(&s.abort_flag, p.status, split);
     }
   } else if (warp == 1) {
     // --------------------------------------------------------------- MMAs ----
@@ -842,14 +855,14 @@ mm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
       int it = 0;
       for (int w = first; ok && w < total; w += step, ++it) {
         const uint32_t acc = tmem + (uint32_t)(it & 1) * C::kAccCols;
-        if (!wait_cluster(&s.acc_empty[it & 1], ((uint32_t)(it >> 1) & 1u) ^ 1u, &s.abort_flag)) {
-          set_abort(&s.abort_flag, p.status);
+        if (!wait_cluster(&s.acc_empty[it & 1], ((uint32_t)(it >> 1) & 1u) ^ 1u, &s.abort_flag, p.wait_ns)) {
+          set_abort(&s.abort_flag, p.status, split);
           break;
         }
         tc_fence_after();
         for (int k = k0; k < k1; ++k) {
-          if (!wait_cluster(&s.full[stage], phase, &s.abort_flag)) {
-            set_abort(&s.abort_flag, p.status);
+          if (!wait_cluster(&s.full[stage], phase, &s.abort_flag, p.wait_ns)) {
+            set_abort(&s.abort_flag, p.status, split);
             ok = false;
             break;
           }
@@ -868,7 +881,7 @@ mm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
       }
       // every tensor-core operation is done before the memories are given back
       tc_commit(&s.drain);
-      if (!mbar_wait(&s.drain, 0)) set_abort(&s.abort_flag, p.status);
+      if (!mbar_wait(&s.drain, 0)) set_abort(&s.abort_flag, p.status, split);
     }
   } else if (warp >= 4) {
     // ----------------------------------------------------------- epilogue ----
@@ -879,9 +892,9 @@ mm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
     for (int w = first; w < total; w += step, ++it) {
       const Tile t = tile_at<kMode>(p, w, kTok, kHalf);
       if (split == 1) {                      // each warp by itself
-        const bool got = wait_cluster(&s.acc_full[it & 1], (uint32_t)(it >> 1) & 1u, &s.abort_flag);
+        const bool got = wait_cluster(&s.acc_full[it & 1], (uint32_t)(it >> 1) & 1u, &s.abort_flag, p.wait_ns);
         if (__any_sync(0xffffffffu, !got)) {
-          set_abort(&s.abort_flag, p.status);
+          set_abort(&s.abort_flag, p.status, split);
           break;
         }
         tc_fence_after();
@@ -893,11 +906,11 @@ mm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
         if (lane == 0) mbar_arrive(&s.acc_empty[it & 1]);
         continue;
       }
-      bool got = wait_cluster(&s.acc_full[it & 1], (uint32_t)(it >> 1) & 1u, &s.abort_flag);
+      bool got = wait_cluster(&s.acc_full[it & 1], (uint32_t)(it >> 1) & 1u, &s.abort_flag, p.wait_ns);
       // the tile before this one has been read by every CTA of the cluster
-      if (it > 0) got = got && wait_cluster(&s.part_empty, (uint32_t)(it - 1) & 1u, &s.abort_flag);
+      if (it > 0) got = got && wait_cluster(&s.part_empty, (uint32_t)(it - 1) & 1u, &s.abort_flag, p.wait_ns);
       if (__any_sync(0xffffffffu, !got)) {
-        set_abort(&s.abort_flag, p.status);
+        set_abort(&s.abort_flag, p.status, split);
         break;
       }
       tc_fence_after();
@@ -915,9 +928,9 @@ mm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.acc_empty[it & 1]);
       if (lane < split) mbar_arrive_rank_release(&s.part_full, lane);
-      const bool all = wait_cluster(&s.part_full, (uint32_t)it & 1u, &s.abort_flag);
+      const bool all = wait_cluster(&s.part_full, (uint32_t)it & 1u, &s.abort_flag, p.wait_ns);
       if (__any_sync(0xffffffffu, !all)) {
-        set_abort(&s.abort_flag, p.status);
+        set_abort(&s.abort_flag, p.status, split);
         break;
       }
       const int col = t.b0 + 4 * lane;

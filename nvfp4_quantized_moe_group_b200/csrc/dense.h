@@ -71,8 +71,10 @@ struct MmArgs {
   const void* residual;  // [rows][J] or nullptr, the operands' type
   void* z_out;           // [rows][J] or nullptr: the sums with the bias, before the activation
   uint32_t* status;
+  uint64_t wait_ns;      // limit of each bounded wait, a millisecond at least
+  int skip_loads;        // test hook: the CTA blockIdx.x + 1 that brings in no operands (0: none)
   int reset_status;      // The product is its call's first kernel: its first CTA clears the status word as it
-                         // starts.  Another CTA can raise a bit 1.5 s after its own start at the earliest
+                         // starts.  Another CTA can raise a bit a wait limit after its own start at the earliest
                          // (an exhausted wait is the only cause).
   int late_wait;         // The previous kernel of the stream is not one this product depends on, and has
                          // itself waited for those it does: it may run beside that kernel, and waits
