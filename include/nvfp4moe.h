@@ -605,7 +605,8 @@ NVFP4MOE_API int nvfp4moe_grouped_mm_backward(int32_t dtype, const void* dy, con
  * nvfp4moe_linear_backward, with dy [M][N] the gradient of y and z as z_out saved it (may be NULL
  * without an activation); the gradient of residual is dy itself:
  *   dz = dy act'(z) in FP32, rounded to dtype as the operand of the two products (dy itself
- *        without an activation)
+ *        without an activation); act' at z = -inf and inf, which z_out holds where a sum passed its
+ *        type's range, is 0 and 1
  *   dx  out [M][K] or NULL: dz W;   dw out [N][K] or NULL: dz^T x, dw_dtype as above;
  *   db  out [N] FP32 or NULL: the column sums of the unrounded dz.
  *   At least one of dx, dw, db; x may be NULL without dw, w without dx.
