@@ -52,13 +52,6 @@ __device__ __forceinline__ float to_f32(typename Elem<kType>::T v) {
   else return __uint_as_float((uint32_t)v << 16);
 }
 
-template <int kType>
-__device__ __forceinline__ typename Elem<kType>::T from_f32(float v) {
-  if constexpr (kType == NVFP4MOE_FP32) return v;
-  else if constexpr (kType == NVFP4MOE_FP16) return __half_as_ushort(__float2half_rn(v));
-  else return __bfloat16_as_ushort(__float2bfloat16_rn(v));
-}
-
 // Sums of kN values over the CTA's threads (one group), in every thread.  s: kN * 32 floats that no
 // other thread still reads (callers alternate two buffers).
 template <int kN>
