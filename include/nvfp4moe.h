@@ -584,7 +584,7 @@ enum {
  *   dx       out [M][K] or NULL: dx[i] = dy[i] W_e (rows outside the segments are not written)
  *   dw       out [E][N][K] or NULL: dW_e = sum over the segment's rows of dy[i]^T x[i], zero for an
  *            empty segment; dw_dtype is dtype or NVFP4MOE_FP32
- *   x may be NULL without dw, w without dx; dx and dw not both NULL (else NVFP4MOE_ERR_ARG).
+ *   x may be NULL without dw, w without dx; dx and dw not both NULL unless M = 0 (else NVFP4MOE_ERR_ARG).
  *   Values outside the segments never enter a sum, whatever they are. */
 NVFP4MOE_API size_t nvfp4moe_grouped_mm_workspace_bytes(int32_t E);
 NVFP4MOE_API int nvfp4moe_grouped_mm(int32_t dtype, const void* x, int64_t M, int32_t K, const void* w, int32_t E,
@@ -609,7 +609,7 @@ NVFP4MOE_API int nvfp4moe_grouped_mm_backward(int32_t dtype, const void* dy, con
  *        type's range, is 0 and 1
  *   dx  out [M][K] or NULL: dz W;   dw out [N][K] or NULL: dz^T x, dw_dtype as above;
  *   db  out [N] FP32 or NULL: the column sums of the unrounded dz.
- *   At least one of dx, dw, db; x may be NULL without dw, w without dx.
+ *   At least one of dx, dw, db unless M = 0; x may be NULL without dw, w without dx.
  * M = 0 leaves nothing to do forward; backward it writes zeros to dw and db. */
 NVFP4MOE_API size_t nvfp4moe_linear_workspace_bytes(int64_t M, int32_t K, int32_t N);
 NVFP4MOE_API int nvfp4moe_linear(int32_t dtype, const void* x, int64_t M, int32_t K, const void* w, int32_t N,

@@ -1764,7 +1764,8 @@ int nvfp4moe_grouped_mm_backward(int32_t dtype, const void* dy, const void* x, c
   g_launches = 0;
   if (!product_type(dtype) || (dw != nullptr && dw_dtype != dtype && dw_dtype != NVFP4MOE_FP32)) return NVFP4MOE_ERR_ARG;
   if (!product_shape(M, K, N, E)) return NVFP4MOE_ERR_SHAPE;
-  if ((dx == nullptr && dw == nullptr) || offsets == nullptr || ws == nullptr) return NVFP4MOE_ERR_ARG;
+  // without rows dx has no elements, so its pointer says nothing
+  if ((M > 0 && dx == nullptr && dw == nullptr) || offsets == nullptr || ws == nullptr) return NVFP4MOE_ERR_ARG;
   if (M > 0 && (dy == nullptr || (dw != nullptr && x == nullptr) || (dx != nullptr && w == nullptr)))
     return NVFP4MOE_ERR_ARG;
   if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(w, 16) || !aligned(dx, 16) || !aligned(dw, 16) ||
@@ -1842,7 +1843,7 @@ int nvfp4moe_linear_backward(int32_t dtype, const void* dy, const void* x, const
       (dw != nullptr && dw_dtype != dtype && dw_dtype != NVFP4MOE_FP32))
     return NVFP4MOE_ERR_ARG;
   if (!product_shape(M, K, N, 1)) return NVFP4MOE_ERR_SHAPE;
-  if ((dx == nullptr && dw == nullptr && db == nullptr) || ws == nullptr) return NVFP4MOE_ERR_ARG;
+  if ((M > 0 && dx == nullptr && dw == nullptr && db == nullptr) || ws == nullptr) return NVFP4MOE_ERR_ARG;
   if (M > 0 && (dy == nullptr || (act != NVFP4MOE_ACT_NONE && z == nullptr) || (dw != nullptr && x == nullptr) ||
                 (dx != nullptr && w == nullptr)))
     return NVFP4MOE_ERR_ARG;
