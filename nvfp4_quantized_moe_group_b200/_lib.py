@@ -885,18 +885,32 @@ def grouped_mm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, out: tor
     return out
 
 
-def grouped_mm_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
+def _backward_operands(M: int, x, w, dx_wanted: bool, dw_wanted: bool):
+    if dx_wanted and w is None:
+        raise ValueError("dx needs w")
+    if dw_wanted and x is None and (M > 0 or w is None):
+        raise ValueError("dw needs x")
+
+
+def grouped_mm_backward(dy: torch.Tensor, x: torch.Tensor | None, w: torch.Tensor | None, offsets: torch.Tensor,
                         need_dx: bool = True, need_dw: bool = True, dw_dtype: torch.dtype | None = None,
                         dx: torch.Tensor | None = None, dw: torch.Tensor | None = None, ws=None, stream=None):
     """Gradients of grouped_mm (nvfp4moe_grouped_mm_backward): dy [M, N] -> (dx [M, K], dw [E, N, K]),
-    None for the one not needed.  ``dx`` / ``dw``: where to write them; ``dw_dtype``: the type of a
-    new dw (x's, or torch.float32)."""
+    None for the one not needed.  x may be None without dw, w without dx.  ``dx`` / ``dw``: where to
+    write them; ``dw_dtype``: the type of a new dw (x's, or torch.float32)."""
     dt = _dtype_of(dy, "dy", _HALF)
     M = _rows(dy, "dy", min_rows=0)
     N = int(dy.shape[1])
-    if not isinstance(w, torch.Tensor) or w.dim() != 3:
-        raise TypeError("w must be a 3-D tensor")
-    E, K = int(w.shape[0]), int(w.shape[2])
+    _backward_operands(M, x, w, need_dx or dx is not None, need_dw or dw is not None)
+    if w is not None:
+        if not isinstance(w, torch.Tensor) or w.dim() != 3:
+            raise TypeError("w must be a 3-D tensor")
+        E, K = int(w.shape[0]), int(w.shape[2])
+    else:
+        if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1:
+            raise TypeError("offsets must be a 1-D tensor")
+        _rows(x, "x", min_rows=0)
+        E, K = int(offsets.shape[0]) - 1, int(x.shape[1])
     wt = _dw_dtype(dw.dtype if isinstance(dw, torch.Tensor) and dw_dtype is None else dw_dtype, dt)
     _require((dy, "dy", dt, None), (x, "x", dt, (M, K)), (w, "w", dt, (E, N, K)),
              (offsets, "offsets", torch.int32, (E + 1,)), (dx, "dx", dt, (M, K)), (dw, "dw", wt, (E, N, K)),
@@ -949,20 +963,28 @@ def linear_backward_workspace_bytes(M: int, K: int, N: int) -> int:
     return int(lib().nvfp4moe_linear_backward_workspace_bytes(int(M), int(K), int(N)))
 
 
-def linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, z: torch.Tensor | None = None,
+def linear_backward(dy: torch.Tensor, x: torch.Tensor | None, w: torch.Tensor | None, z: torch.Tensor | None = None,
                     act: str = "none", bias: bool = False, need_dx: bool = True, need_dw: bool = True,
                     dw_dtype: torch.dtype | None = None, dx: torch.Tensor | None = None,
                     dw: torch.Tensor | None = None, ws=None, stream=None):
     """Gradients of linear (nvfp4moe_linear_backward): dy [M, N] and the saved pre-activation z ->
-    (dx [M, K], dw [N, K], db [N] float32), None for those not needed (``bias``: db is).  The
-    gradient of the residual is dy."""
+    (dx [M, K], dw [N, K], db [N] float32), None for those not needed (``bias``: db is).  x may be
+    None without dw, w without dx.  The gradient of the residual is dy."""
     dt = _dtype_of(dy, "dy", _HALF)
     a = _activation(act)
     if a != 0 and z is None:
         raise ValueError(f"act {act!r} needs the pre-activation z")
     M = _rows(dy, "dy", min_rows=0)
     N = int(dy.shape[1])
-    K = int(w.shape[1]) if _rows(w, "w") else 0
+    _backward_operands(M, x, w, need_dx or dx is not None, need_dw or dw is not None)
+    if w is not None:
+        _rows(w, "w")
+        K = int(w.shape[1])
+    elif x is not None:
+        _rows(x, "x", min_rows=0)
+        K = int(x.shape[1])
+    else:
+        K = 8                                  # db alone: no product, any K the library takes
     wt = _dw_dtype(dw.dtype if isinstance(dw, torch.Tensor) and dw_dtype is None else dw_dtype, dt)
     _require((dy, "dy", dt, None), (x, "x", dt, (M, K)), (w, "w", dt, (N, K)), (z, "z", dt, (M, N)),
              (dx, "dx", dt, (M, K)), (dw, "dw", wt, (N, K)), (ws, "ws", torch.uint8, None))
