@@ -553,6 +553,9 @@ NVFP4MOE_API int nvfp4moe_forward_fp8(const nvfp4moe_fp8_experts* experts, const
  * pointers, dense row-major tensors, errors, status word, workspaces).  Tensor pointers are
  * 16-byte aligned unless stated otherwise, and outputs do not overlap inputs unless stated.
  *
+ * The *_workspace_bytes functions never fall as the rows (M, rows) grow: a workspace for the most rows serves any fewer
+ * of the same sizes.
+ *
  * Products take BF16 or FP16 operands, accumulate in FP32 on the tensor cores and round each
  * result once.  Limits: 0 <= M < 2^25, K and N multiples of 8 from 8 to 2^19, 1 <= E <= 1024,
  * M * K, M * N and E * K * N below 2^40; outside them NVFP4MOE_ERR_SHAPE. */

@@ -414,14 +414,6 @@ struct ProductWs {
   size_t bytes;
 };
 
-// Floats of the parts of a row product [M][J] run as `plan`, and of a weight gradient [E][I][J].
-size_t row_part_floats(const MmPlan& plan, int64_t M, int32_t J) {
-  return plan.pair && plan.split > 1 ? (size_t)plan.split * (size_t)(M * J) : 0;
-}
-size_t wgrad_part_floats(int split, int32_t E, int32_t I, int32_t J) {
-  return split > 1 ? (size_t)split * (size_t)E * (size_t)((int64_t)I * J) : 0;
-}
-
 ProductWs carve_product(void* ws, int32_t E, size_t row_floats, size_t wgrad_floats) {
   Carver c(ws);
   ProductWs p{};
@@ -1755,7 +1747,7 @@ int nvfp4moe_grouped_mm(int32_t dtype, const void* x, int64_t M, int32_t K, cons
 
 size_t nvfp4moe_grouped_mm_backward_workspace_bytes(int64_t M, int32_t K, int32_t E, int32_t N) {
   if (!product_shape(M, K, N, E)) return 0;
-  return carve_product(nullptr, E, 0, wgrad_part_floats(mm_wgrad_split(M, E, N, K), E, N, K)).bytes;
+  return carve_product(nullptr, E, 0, mm_wgrad_part_floats(M, E, N, K)).bytes;
 }
 
 int nvfp4moe_grouped_mm_backward(int32_t dtype, const void* dy, const void* x, const void* w, int64_t M, int32_t K,
@@ -1772,7 +1764,7 @@ int nvfp4moe_grouped_mm_backward(int32_t dtype, const void* dy, const void* x, c
       !aligned(offsets, 4) || !aligned(ws, kAlign))
     return NVFP4MOE_ERR_ARG;
   const int split = mm_wgrad_split(M, E, N, K);
-  const ProductWs p = carve_product(ws, E, 0, wgrad_part_floats(split, E, N, K));
+  const ProductWs p = carve_product(ws, E, 0, mm_wgrad_part_floats(M, E, N, K));
   if (ws_bytes < p.bytes) return NVFP4MOE_ERR_WORKSPACE;
   const int st = check_device();
   if (st != NVFP4MOE_OK) return st;
@@ -1789,7 +1781,7 @@ int nvfp4moe_grouped_mm_backward(int32_t dtype, const void* dy, const void* x, c
 
 size_t nvfp4moe_linear_workspace_bytes(int64_t M, int32_t K, int32_t N) {
   if (!product_shape(M, K, N, 1)) return 0;
-  return carve_product(nullptr, 1, row_part_floats(mm_plan(M, 1, N, K, false), M, N), 0).bytes;
+  return carve_product(nullptr, 1, mm_row_part_floats(M, N, K), 0).bytes;
 }
 
 int nvfp4moe_linear(int32_t dtype, const void* x, int64_t M, int32_t K, const void* w, int32_t N, const float* bias,
@@ -1802,7 +1794,7 @@ int nvfp4moe_linear(int32_t dtype, const void* x, int64_t M, int32_t K, const vo
       !aligned(z_out, 16) || !aligned(ws, kAlign))
     return NVFP4MOE_ERR_ARG;
   const MmPlan plan = mm_plan(M, 1, N, K, false);
-  const ProductWs p = carve_product(ws, 1, row_part_floats(plan, M, N), 0);
+  const ProductWs p = carve_product(ws, 1, mm_row_part_floats(M, N, K), 0);
   if (ws_bytes < p.bytes) return NVFP4MOE_ERR_WORKSPACE;
   const int st = check_device();
   if (st != NVFP4MOE_OK) return st;
@@ -1830,9 +1822,7 @@ int nvfp4moe_linear(int32_t dtype, const void* x, int64_t M, int32_t K, const vo
 
 size_t nvfp4moe_linear_backward_workspace_bytes(int64_t M, int32_t K, int32_t N) {
   if (!product_shape(M, K, N, 1)) return 0;
-  return carve_linear_backward(nullptr, M, N, row_part_floats(mm_plan(M, 1, K, N, false), M, K),
-                               wgrad_part_floats(mm_wgrad_split(M, 1, N, K), 1, N, K))
-      .bytes;
+  return carve_linear_backward(nullptr, M, N, mm_row_part_floats(M, K, N), mm_wgrad_part_floats(M, 1, N, K)).bytes;
 }
 
 int nvfp4moe_linear_backward(int32_t dtype, const void* dy, const void* x, const void* w, const void* z, int64_t M,
@@ -1852,8 +1842,7 @@ int nvfp4moe_linear_backward(int32_t dtype, const void* dy, const void* x, const
     return NVFP4MOE_ERR_ARG;
   const MmPlan plan = mm_plan(M, 1, K, N, false);
   const int split = mm_wgrad_split(M, 1, N, K);
-  const ProductWs p =
-      carve_linear_backward(ws, M, N, row_part_floats(plan, M, K), wgrad_part_floats(split, 1, N, K));
+  const ProductWs p = carve_linear_backward(ws, M, N, mm_row_part_floats(M, K, N), mm_wgrad_part_floats(M, 1, N, K));
   if (ws_bytes < p.bytes) return NVFP4MOE_ERR_WORKSPACE;
   const int st = check_device();
   if (st != NVFP4MOE_OK) return st;
@@ -1907,7 +1896,7 @@ int nvfp4moe_layer_norm(int32_t dtype, const void* x, int64_t rows, int32_t cols
 
 size_t nvfp4moe_layer_norm_backward_workspace_bytes(int64_t rows, int32_t cols) {
   if (rows < 0 || rows >= ((int64_t)1 << 31) || cols < 1 || cols > kNormMaxCols) return 0;
-  return align_up((size_t)(rows > 0 ? norm_backward_parts(rows, cols) : 1) * 2 * (size_t)cols * sizeof(float));
+  return align_up((size_t)(rows > 0 ? norm_backward_parts(rows) : 1) * 2 * (size_t)cols * sizeof(float));
 }
 
 int nvfp4moe_layer_norm_backward(int32_t dtype, const void* dy, const void* x, int64_t rows, int32_t cols,

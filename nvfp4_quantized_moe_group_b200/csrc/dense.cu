@@ -1262,6 +1262,23 @@ int mm_wgrad_split(int64_t rows, int E, int I, int J) {
   return best;
 }
 
+// At most kPairs / tiles and steps / 4 parts, as the plans; tiles x parts are at most kPairs, so the parts never hold
+// more than that many tiles.
+size_t mm_row_part_floats(int64_t rows, int J, int R) {
+  const int64_t across = ((int64_t)J + kPairTile - 1) / kPairTile, steps = ((int64_t)R + kBK - 1) / kBK;
+  const int64_t most = kPairs / across < steps / 4 ? kPairs / across : steps / 4;
+  if (most < 2) return 0;
+  const int64_t all = (int64_t)kPairs * kPairTile * kPairTile, by_rows = most * rows * (int64_t)J;
+  return (size_t)(by_rows < all ? by_rows : all);
+}
+
+size_t mm_wgrad_part_floats(int64_t rows, int E, int I, int J) {
+  const int64_t tiles = (int64_t)E * ((I + kPairTile - 1) / kPairTile) * ((J + kPairTile - 1) / kPairTile);
+  const int64_t steps = (rows + (int64_t)E * kBK - 1) / ((int64_t)E * kBK);
+  const int64_t most = kPairs / tiles < steps / 4 ? kPairs / tiles : steps / 4;
+  return most < 2 ? 0 : (size_t)(most * E * I * (int64_t)J);
+}
+
 cudaError_t launch_mm_table(const int32_t* offsets, int E, int64_t rows, int tile_rows, const MmTable& t,
                             WsHeader* hdr, const MmWgradOperands* w, cudaStream_t stream) {
   MmSegMaps maps{};

@@ -53,6 +53,10 @@ struct MmPlan {
 MmPlan mm_plan(int64_t rows, int E, int J, int R, bool ragged);
 // In how many parts wgrad's pairs share the token rows (of each segment) of a tile.
 int mm_wgrad_split(int64_t rows, int E, int I, int J);
+// FP32 parts that workspaces hold for a dense row product and for wgrad: enough for every plan of up to `rows` rows,
+// so that a workspace for many rows serves fewer (which are the ones that share tiles among more pairs).
+size_t mm_row_part_floats(int64_t rows, int J, int R);
+size_t mm_wgrad_part_floats(int64_t rows, int E, int I, int J);
 
 struct MmArgs {
   const int32_t* seg;    // as in MmTable; nullptr: one segment, all `rows` rows

@@ -725,10 +725,11 @@ cudaError_t backward_type(const NormArgs& a, int ctas, cudaStream_t stream) {
 
 }  // namespace
 
-// The workspace is sized without the element type: the larger grid of the two vector lengths.
-int norm_backward_parts(int64_t rows, int cols) {
-  const int n8 = backward_ctas(rows, cols, 8), n4 = backward_ctas(rows, cols, 4);
-  return n8 > n4 ? n8 : n4;
+// As many as grid_of can give for up to `rows` rows of any width and type: few rows take a CTA each, more rows
+// share CTAs, so the grid of more rows may be the smaller one.
+int norm_backward_parts(int64_t rows) {
+  const int most = num_sms();
+  return (int)(rows < most ? (rows + 7) / 8 * 8 < most ? (rows + 7) / 8 * 8 : most : most);
 }
 
 cudaError_t launch_norm_forward(const NormArgs& a, int32_t* launches, cudaStream_t stream) {

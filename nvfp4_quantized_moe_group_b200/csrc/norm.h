@@ -27,8 +27,8 @@ struct NormArgs {
   int dtype;             // NVFP4MOE_BF16 / _FP16 / _FP32
 };
 
-// CTAs of the backward pass (the most: what the workspace is sized for).
-int norm_backward_parts(int64_t rows, int cols);
+// The most CTAs that the backward pass of up to `rows` rows takes: what the workspace is sized for.
+int norm_backward_parts(int64_t rows);
 cudaError_t launch_norm_forward(const NormArgs& a, int* launches, cudaStream_t stream);
 cudaError_t launch_norm_backward(const NormArgs& a, int* launches, cudaStream_t stream);
 
