@@ -7,6 +7,7 @@ Loading fails loudly when the library is missing: there is no fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -829,13 +830,25 @@ def _dtype_of(t, name: str, allowed) -> torch.dtype:
 _HALF = (torch.bfloat16, torch.float16)
 
 
+_NO_STREAM = contextlib.nullcontext()
+
+
+def _allocating(stream):
+    """Where a call on another stream takes its outputs and workspace from: that stream's memory.  A block of the current
+    stream's could have been given back with kernels of the current stream still to run on it, which nothing makes
+    the other stream wait for."""
+    return _NO_STREAM if stream is None else torch.cuda.stream(stream)
+
+
 def _keep(stream, *tensors):
-    """Outputs and workspaces come from the current stream's allocator: on another stream they stay
-    reserved until that stream has passed the call, also when the caller drops them before."""
+    """The tensors of a call on another stream stay reserved until both that stream and the current one, which
+    may use the outputs, have passed what is queued when the caller drops them."""
     if stream is not None:
+        current = torch.cuda.current_stream()
         for t in tensors:
             if t is not None:
                 t.record_stream(stream)
+                t.record_stream(current)
 
 
 def _activation(act: str) -> int:
@@ -875,10 +888,11 @@ def grouped_mm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, out: tor
     E, N = int(w.shape[0]), int(w.shape[1])
     _require((x, "x", dt, None), (w, "w", dt, (E, N, K)), (offsets, "offsets", torch.int32, (E + 1,)),
              (out, "out", dt, (M, N)), (ws, "ws", torch.uint8, None))
-    if out is None:
-        out = x.new_empty((M, N))
-    if ws is None:
-        ws = _workspace(grouped_mm_workspace_bytes(E), x.device)
+    with _allocating(stream):
+        if out is None:
+            out = x.new_empty((M, N))
+        if ws is None:
+            ws = _workspace(grouped_mm_workspace_bytes(E), x.device)
     _check(lib().nvfp4moe_grouped_mm(DTYPES[dt], _ptr(x), M, K, _ptr(w), E, N, _ptr(offsets), _ptr(out), _ptr(ws),
                                      ws.numel(), _stream(stream)), "nvfp4moe_grouped_mm")
     _keep(stream, out, ws)
@@ -915,12 +929,13 @@ def grouped_mm_backward(dy: torch.Tensor, x: torch.Tensor | None, w: torch.Tenso
     _require((dy, "dy", dt, None), (x, "x", dt, (M, K)), (w, "w", dt, (E, N, K)),
              (offsets, "offsets", torch.int32, (E + 1,)), (dx, "dx", dt, (M, K)), (dw, "dw", wt, (E, N, K)),
              (ws, "ws", torch.uint8, None))
-    if dx is None and need_dx:
-        dx = dy.new_empty((M, K))
-    if dw is None and need_dw:
-        dw = dy.new_empty((E, N, K), dtype=wt)
-    if ws is None:
-        ws = _workspace(grouped_mm_backward_workspace_bytes(M, K, E, N), dy.device)
+    with _allocating(stream):
+        if dx is None and need_dx:
+            dx = dy.new_empty((M, K))
+        if dw is None and need_dw:
+            dw = dy.new_empty((E, N, K), dtype=wt)
+        if ws is None:
+            ws = _workspace(grouped_mm_backward_workspace_bytes(M, K, E, N), dy.device)
     _check(lib().nvfp4moe_grouped_mm_backward(DTYPES[dt], _ptr(dy), _ptr(x), _ptr(w), M, K, E, N, _ptr(offsets),
                                               _ptr(dx), _ptr(dw), DTYPES[wt], _ptr(ws), ws.numel(), _stream(stream)),
            "nvfp4moe_grouped_mm_backward")
@@ -947,11 +962,12 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None, a
     N = _rows(w, "w")
     _require((x, "x", dt, None), (w, "w", dt, (N, K)), (bias, "bias", torch.float32, (N,)),
              (residual, "residual", dt, (M, N)), (out, "out", dt, (M, N)), (ws, "ws", torch.uint8, None))
-    if out is None:
-        out = x.new_empty((M, N))
-    z = torch.empty_like(out) if save_z else None
-    if ws is None:
-        ws = _workspace(linear_workspace_bytes(M, K, N), x.device)
+    with _allocating(stream):
+        if out is None:
+            out = x.new_empty((M, N))
+        z = torch.empty_like(out) if save_z else None
+        if ws is None:
+            ws = _workspace(linear_workspace_bytes(M, K, N), x.device)
     _check(lib().nvfp4moe_linear(DTYPES[dt], _ptr(x), M, K, _ptr(w), N, _ptr(bias), a, _ptr(residual), _ptr(z),
                                  _ptr(out), _ptr(ws), ws.numel(), _stream(stream)), "nvfp4moe_linear")
     _keep(stream, out, z, ws)
@@ -989,13 +1005,14 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor | None, w: torch.Tensor | 
     _require((dy, "dy", dt, None), (x, "x", dt, (M, K)), (w, "w", dt, (N, K)), (z, "z", dt, (M, N)),
              (dx, "dx", dt, (M, K)), (dw, "dw", wt, (N, K)), (ws, "ws", torch.uint8, None))
     dev = dy.device
-    if dx is None and need_dx:
-        dx = dy.new_empty((M, K))
-    if dw is None and need_dw:
-        dw = dy.new_empty((N, K), dtype=wt)
-    db = dy.new_empty(N, dtype=torch.float32) if bias else None
-    if ws is None:
-        ws = _workspace(linear_backward_workspace_bytes(M, K, N), dev)
+    with _allocating(stream):
+        if dx is None and need_dx:
+            dx = dy.new_empty((M, K))
+        if dw is None and need_dw:
+            dw = dy.new_empty((N, K), dtype=wt)
+        db = dy.new_empty(N, dtype=torch.float32) if bias else None
+        if ws is None:
+            ws = _workspace(linear_backward_workspace_bytes(M, K, N), dev)
     _check(lib().nvfp4moe_linear_backward(DTYPES[dt], _ptr(dy), _ptr(x), _ptr(w), _ptr(z), M, K, N, a, _ptr(dx),
                                           _ptr(dw), DTYPES[wt], _ptr(db), _ptr(ws), ws.numel(), _stream(stream)),
            "nvfp4moe_linear_backward")
@@ -1020,10 +1037,11 @@ def layer_norm(x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.T
     cols = int(x.shape[1])
     _require((x, "x", dt, None), (gamma, "gamma", torch.float32, (cols,)), (beta, "beta", torch.float32, (cols,)),
              (out, "out", dt, (rows, cols)))
-    if out is None:
-        out = torch.empty_like(x)
-    mean = x.new_empty(rows, dtype=torch.float32) if stats and not rms else None
-    rstd = x.new_empty(rows, dtype=torch.float32) if stats else None
+    with _allocating(stream):
+        if out is None:
+            out = torch.empty_like(x)
+        mean = x.new_empty(rows, dtype=torch.float32) if stats and not rms else None
+        rstd = x.new_empty(rows, dtype=torch.float32) if stats else None
     _check(lib().nvfp4moe_layer_norm(DTYPES[dt], _ptr(x), rows, cols, _ptr(gamma), _ptr(beta), float(eps),
                                      int(bool(rms)), _ptr(out), _ptr(mean), _ptr(rstd), _stream(stream)),
            "nvfp4moe_layer_norm")
@@ -1053,12 +1071,13 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor |
     dev = dy.device
     if need_params is None:
         need_params = gamma is not None
-    if dx is None:
-        dx = torch.empty_like(dy)
-    dgamma = dy.new_empty(cols, dtype=torch.float32) if need_params else None
-    dbeta = torch.empty_like(dgamma) if need_params and not rms else None
-    if ws is None and need_params:
-        ws = _workspace(layer_norm_backward_workspace_bytes(rows, cols), dev)
+    with _allocating(stream):
+        if dx is None:
+            dx = torch.empty_like(dy)
+        dgamma = dy.new_empty(cols, dtype=torch.float32) if need_params else None
+        dbeta = torch.empty_like(dgamma) if need_params and not rms else None
+        if ws is None and need_params:
+            ws = _workspace(layer_norm_backward_workspace_bytes(rows, cols), dev)
     _check(lib().nvfp4moe_layer_norm_backward(DTYPES[dt], _ptr(dy), _ptr(x), rows, cols, _ptr(gamma),
                                               None if rms else _ptr(mean), _ptr(rstd), int(bool(rms)), _ptr(dx),
                                               _ptr(dgamma), _ptr(dbeta), _ptr(ws), ws.numel() if ws is not None else 0,
