@@ -118,10 +118,16 @@ __device__ __forceinline__ void store_rank(int* dst, uint64_t* bar, uint32_t ran
                : "memory");
 }
 
-// Reports a wait that ran out and ends those of every CTA of the cluster (each is there until the barrier at the
-// kernel's end, which this thread has still to pass).
-__device__ __forceinline__ void set_abort(int* flag, uint32_t* status, int ctas) {
+__device__ __forceinline__ void set_abort(int* flag, uint32_t* status) {
   raise_status(status, kStatusTimeout);
+  *reinterpret_cast<volatile int*>(flag) = 1;
+}
+
+// Before a warp's last barrier of the cluster: a CTA that gave up ends the waits of its cluster's others too (they are
+// there until that barrier).  Done here once, not where a wait runs out: in every such place it was code enough
+// to cost short calls their instruction fetches (both gradients of 13 experts, 1531 rows, 520 x 776: 33.4 us, here 32.4).
+__device__ __forceinline__ void spread_abort(int* flag, int ctas) {
+  if (*reinterpret_cast<volatile int*>(flag) == 0) return;
   for (int r = 0; r < ctas; ++r)
     asm volatile("st.relaxed.cluster.shared::cluster.b32 [%0], %1;" ::"r"(map_rank(smem_u32(flag), (uint32_t)r)), "r"(1)
                  : "memory");
@@ -443,7 +449,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         int w;
         if (rank == 0) {
           if (!wait_cluster(&s.work_empty[slot], ((uint32_t)(it / kWorkRing) & 1u) ^ 1u, &s.abort_flag, p.wait_ns)) {
-            set_abort(&s.abort_flag, p.status, 2);
+            set_abort(&s.abort_flag, p.status);
             ok = false;
             break;
           }
@@ -462,7 +468,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
           mbar_arrive_expect_tx(&s.work_full[slot], 4);
           w = next_tile<false>(s, it, lane, p.wait_ns);
           if (w == -2) {
-            set_abort(&s.abort_flag, p.status, 2);
+            set_abort(&s.abort_flag, p.status);
             ok = false;
           }
         }
@@ -491,7 +497,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         const uint32_t b_bytes = (half > 64 ? kHalf : half > 32 ? 64 : 32) * kBK * 2;
         for (int k = 0; k < t.steps; ++k) {
           if (!wait_cluster(&s.empty[stage], phase ^ 1u, &s.abort_flag, p.wait_ns)) {
-            set_abort(&s.abort_flag, p.status, 2);
+            set_abort(&s.abort_flag, p.status);
             ok = false;
             break;
           }
@@ -519,7 +525,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
       // of a CTA that has exited, or of the next kernel's.  It also shows that every copy has landed.
       for (int i = 0; ok && i < kPairStages; ++i) {
         if (!wait_cluster(&s.empty[stage], phase ^ 1u, &s.abort_flag, p.wait_ns)) {
-          set_abort(&s.abort_flag, p.status, 2);
+          set_abort(&s.abort_flag, p.status);
           ok = false;
         }
         if (++stage == kPairStages) { stage = 0; phase ^= 1u; }
@@ -540,7 +546,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
       for (int n = 0; ok; ++n) {
         const int w = next_tile<false>(s, n, lane, p.wait_ns);
         if (w < 0) {
-          if (w == -2) set_abort(&s.abort_flag, p.status, 2);
+          if (w == -2) set_abort(&s.abort_flag, p.status);
           break;
         }
         const Tile t = tile_at<kMode>(p, w, tile_i, kPairTile);
@@ -549,13 +555,13 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             idesc_f16(2 * kHalf, kTokens ? pair_columns(t.rows_valid) : kPairTile, p.fp16 != 0, kAMn, kBMn);
         const uint32_t acc = tmem + (uint32_t)(it & 1) * kPairTile;
         if (!wait_cluster(&s.acc_empty[it & 1], ((uint32_t)(it >> 1) & 1u) ^ 1u, &s.abort_flag, p.wait_ns)) {
-          set_abort(&s.abort_flag, p.status, 2);
+          set_abort(&s.abort_flag, p.status);
           break;
         }
         tc_fence_after();
         for (int k = 0; k < t.steps; ++k) {
           if (!wait_cluster(&s.full[stage], phase, &s.abort_flag, p.wait_ns)) {
-            set_abort(&s.abort_flag, p.status, 2);
+            set_abort(&s.abort_flag, p.status);
             ok = false;
             break;
           }
@@ -577,7 +583,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
       }
       // every tensor-core operation of the pair is done before the memories are given back
       tc_commit_pair_local(&s.drain);
-      if (!mbar_wait(&s.drain, 0)) set_abort(&s.abort_flag, p.status, 2);
+      if (!mbar_wait(&s.drain, 0)) set_abort(&s.abort_flag, p.status);
     }
   } else if (warp >= 4) {
     // ----------------------------------------------------------- epilogue ----
@@ -589,7 +595,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     for (int n = 0;; ++n) {
       const int w = next_tile<true>(s, n, lane, p.wait_ns);
       if (w < 0) {
-        if (w == -2) set_abort(&s.abort_flag, p.status, 2);
+        if (w == -2) set_abort(&s.abort_flag, p.status);
         break;
       }
       const Tile t = tile_at<kMode>(p, w, tile_i, kPairTile);
@@ -597,7 +603,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
       if (has_acc) {
         const bool got = wait_cluster(&s.acc_full[it & 1], (uint32_t)(it >> 1) & 1u, &s.abort_flag, p.wait_ns);
         if (__any_sync(0xffffffffu, !got)) {
-          set_abort(&s.abort_flag, p.status, 2);
+          set_abort(&s.abort_flag, p.status);
           break;
         }
         tc_fence_after();
@@ -670,6 +676,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
   }
 
   __syncwarp();
+  spread_abort(&s.abort_flag, 2);
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
@@ -814,7 +821,7 @@ mm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
         const Tile t = tile_at<kMode>(p, w, kTok, kHalf);
         for (int k = k0; k < k1; ++k) {
           if (!wait_cluster(&s.empty[stage], phase ^ 1u, &s.abort_flag, p.wait_ns)) {
-            set_abort(&s.abort_flag, p.status, split);
+            set_abort(&s.abort_flag, p.status);
             ok = false;
             break;
           }
@@ -835,7 +842,7 @@ mm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
       // the MMAs have read every stage: no copy and no arrival of theirs is under way at the exit
       for (int i = 0; ok && i < kStages; ++i) {
         if (!wait_cluster(&s.empty[stage], phase ^ 1u, &s.abort_flag, p.wait_ns)) {
-          set_abort(&s.abort_flag, p.status, split);
+          set_abort(&s.abort_flag, p.status);
           ok = false;
         }
         if (++stage == kStages) { stage = 0; phase ^= 1u; }
@@ -843,7 +850,7 @@ mm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
       // after giving up, the copies at least have landed
       for (int i = 0; !ok && i < kStages; ++i)
         if ((issued >> i) & 1u)
-          if (!mbar_wait(&s.full[i], (issued_par >> i) & 1u)) set_abort(&s.abort_flag, p.status, split);
+          if (!mbar_wait(&s.full[i], (issued_par >> i) & 1u)) set_abort(&s.abort_flag, p.status);
     }
   } else if (warp == 1) {
     // --------------------------------------------------------------- MMAs ----
@@ -856,13 +863,13 @@ mm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
       for (int w = first; ok && w < total; w += step, ++it) {
         const uint32_t acc = tmem + (uint32_t)(it & 1) * C::kAccCols;
         if (!wait_cluster(&s.acc_empty[it & 1], ((uint32_t)(it >> 1) & 1u) ^ 1u, &s.abort_flag, p.wait_ns)) {
-          set_abort(&s.abort_flag, p.status, split);
+          set_abort(&s.abort_flag, p.status);
           break;
         }
         tc_fence_after();
         for (int k = k0; k < k1; ++k) {
           if (!wait_cluster(&s.full[stage], phase, &s.abort_flag, p.wait_ns)) {
-            set_abort(&s.abort_flag, p.status, split);
+            set_abort(&s.abort_flag, p.status);
             ok = false;
             break;
           }
@@ -881,7 +888,7 @@ mm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
       }
       // every tensor-core operation is done before the memories are given back
       tc_commit(&s.drain);
-      if (!mbar_wait(&s.drain, 0)) set_abort(&s.abort_flag, p.status, split);
+      if (!mbar_wait(&s.drain, 0)) set_abort(&s.abort_flag, p.status);
     }
   } else if (warp >= 4) {
     // ----------------------------------------------------------- epilogue ----
@@ -894,7 +901,7 @@ mm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
       if (split == 1) {                      // each warp by itself
         const bool got = wait_cluster(&s.acc_full[it & 1], (uint32_t)(it >> 1) & 1u, &s.abort_flag, p.wait_ns);
         if (__any_sync(0xffffffffu, !got)) {
-          set_abort(&s.abort_flag, p.status, split);
+          set_abort(&s.abort_flag, p.status);
           break;
         }
         tc_fence_after();
@@ -910,7 +917,7 @@ mm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
       // the tile before this one has been read by every CTA of the cluster
       if (it > 0) got = got && wait_cluster(&s.part_empty, (uint32_t)(it - 1) & 1u, &s.abort_flag, p.wait_ns);
       if (__any_sync(0xffffffffu, !got)) {
-        set_abort(&s.abort_flag, p.status, split);
+        set_abort(&s.abort_flag, p.status);
         break;
       }
       tc_fence_after();
@@ -930,7 +937,7 @@ mm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
       if (lane < split) mbar_arrive_rank_release(&s.part_full, lane);
       const bool all = wait_cluster(&s.part_full, (uint32_t)it & 1u, &s.abort_flag, p.wait_ns);
       if (__any_sync(0xffffffffu, !all)) {
-        set_abort(&s.abort_flag, p.status, split);
+        set_abort(&s.abort_flag, p.status);
         break;
       }
       const int col = t.b0 + 4 * lane;
@@ -972,6 +979,7 @@ mm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
   }
 
   __syncwarp();
+  spread_abort(&s.abort_flag, split);
   tc_fence_before();
   if (split > 1) cluster_sync(); else __syncthreads();
   tc_fence_after();
