@@ -30,24 +30,25 @@ __device__ __forceinline__ float act_value(float z) {
   else return z;
 }
 
-// d act / dz; its limits 0 and 1 at infinite z (a saved sum beyond its 16-bit type), where the formulas' second
-// terms are 0 times inf.
+// `limit` where the formula is 0 times inf, and at a NaN, where it is NaN itself.
+__device__ __forceinline__ float or_limit(float v, float limit) { return v == v ? v : limit; }
+
+// d act / dz; its limits 0 and 1 at infinite z (a saved sum beyond its 16-bit type) and where z's square is beyond FP32.
 template <int kAct>
 __device__ __forceinline__ float act_slope(float z) {
   if constexpr (kAct == NVFP4MOE_ACT_RELU) {
     return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
   } else if constexpr (kAct == NVFP4MOE_ACT_SILU) {
     const float p = sigmoid_f(z);
-    return p == 0.0f || p == 1.0f ? p : p * (1.0f + z * (1.0f - p));
+    return or_limit(p * (1.0f + z * (1.0f - p)), p);
   } else if constexpr (kAct == NVFP4MOE_ACT_GELU) {
     const float phi = 0.5f * (1.0f + erff(z * kSqrtHalf)), e = __expf(-0.5f * z * z);
-    return e == 0.0f ? phi : phi + z * e * kInvSqrt2Pi;
+    return or_limit(phi + z * e * kInvSqrt2Pi, phi);
   } else if constexpr (kAct == NVFP4MOE_ACT_GELU_TANH) {
     const float z2 = z * z;
     const float p = sigmoid_f(2.0f * kSqrt2OverPi * (z + 0.044715f * z * z2));
-    // p + z p (1 - p) d(2u)/dz; z2 is inf only where p is 0 or 1
-    if (p == 0.0f || p == 1.0f) return p;
-    return p + z * p * (1.0f - p) * (2.0f * kSqrt2OverPi) * (1.0f + 3.0f * 0.044715f * z2);
+    // p + z p (1 - p) d(2u)/dz
+    return or_limit(p + z * p * (1.0f - p) * (2.0f * kSqrt2OverPi) * (1.0f + 3.0f * 0.044715f * z2), p);
   } else {
     return 1.0f;
   }
