@@ -22,8 +22,8 @@
 // barrier; warp 1 of the first CTA issues the MMAs; warps 4-11 run the epilogue: forward and dgrad
 // transpose 32 x 32 pieces through shared memory, stored by TMA from there (a segment's last rows, which no
 // map can clip, row by row); wgrad, whose rows are never ragged, in 128-byte x 32-row pieces (an expert's few rows make
-// few steps a tile, so wgrad is bound by its output: 64 experts of 128 rows, 5120 x 2560, 468 us, with
-// plain stores 931 us).
+// few steps a tile, so its output counts most: 64 experts of 128 rows, 5120 x 2560, 468 us, with plain stores
+// 931 us; its 1678 MB alone are a fill of 228 us).
 //
 // Ragged ends.  In forward and dgrad, rows behind a segment's end only feed accumulator columns that
 // are not stored.  In wgrad the reduction runs over rows, so the last step of a segment would add
@@ -35,9 +35,10 @@
 // Every wait is bounded; one that runs out raises the timeout bit of the status word and the abort flag of
 // every CTA of its cluster, which wind down together.
 //
-// Measured: 4096 x 5120 x 5120 150 us (1.43 PFLOP/s), 4096 x 20480, K = 5120 with GELU and saved sums 587 us
-// (1.46 PFLOP/s); 64 skewed experts, 32768 rows, 2560 -> 5120 704 to 757 us; both gradients of 32 experts, 8192 rows,
-// 475 us; 32 rows over 64 experts, 5120 -> 2560, 111 us (6.4 TB/s).
+// Measured in a replayed graph, and called for long (at the power cap): 4096 x 5120 x 5120 150 us (1.43 PFLOP/s); 4096 x
+// 20480, K = 5120 with GELU and saved sums 587 to 602 us (by card) and 693 to 731; 64 skewed experts, 32768 rows,
+// 2560 -> 5120 704 to 757 and 845 to 920; both gradients of 32 experts, 8192 rows, 470 to 483 and 564 to 578; 32 rows
+// over 64 experts, 5120 -> 2560, 111 (6.4 TB/s) and 113.
 #include "common.cuh"
 #include "dense.h"
 #include "dense_epilogue.cuh"

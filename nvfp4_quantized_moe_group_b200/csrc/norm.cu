@@ -7,8 +7,9 @@
 //             dgamma = sum_rows dy xh,  dbeta = sum_rows dy
 // (RMS form: mean = 0 throughout, no mean_j(g) term, no beta.)
 //
-// All arithmetic is FP32; the variance is summed from the centred values, so a row's common offset
-// costs no digits.  Both passes are memory bound (2 and 3 values moved per element).
+// All arithmetic is FP32; the variance is summed from the centred values, so a row's common offset costs
+// digits in the mean only (a few units of 2^-24 of the offset).  Both passes are memory bound (2 and 3 values moved
+// per element).
 //
 // One persistent CTA per SM holds several groups of threads; each group takes rows in turn, each
 // thread its own 16-byte vectors of them (32 elements a thread, so that the reductions' fixed cost
@@ -31,8 +32,8 @@
 // ran).  Rows too wide for that keep the column sums in shared memory and read x and dy a second time
 // (from L2).
 //
-// Measured: 32768 x 5120 BF16 forward 139 us (4.8 TB/s), backward 197 us (5.1 TB/s); 8191 x 2571 FP32 forward
-// 36 us (4.7 TB/s); 16 x 5120 forward 3.3 us.
+// Measured in a replayed graph: 32768 x 5120 BF16 forward 137 us (4.9 TB/s), backward 197 us (5.1 TB/s; called 217 to 222);
+// 8191 x 2571 FP32 forward 35 to 36 us (4.8 TB/s); 16 x 5120 forward 3.1 us (called 12).
 #include "activation.cuh"
 #include "common.cuh"
 #include "kernels.h"
