@@ -29,8 +29,8 @@
 // are not stored.  In wgrad the reduction runs over rows, so the last step of a segment would add
 // rows of the next one (or rows never written, where a NaN passes even a zero factor): each
 // segment has tensor maps of its own, built on the device from the offsets, whose row bound makes
-// the loads fill zeros behind its end.  (Zeroing those lines in shared memory before the MMAs
-// cost every tile a cross-CTA fence: 64 skewed experts, 32768 rows, 1011 us.)
+// the loads fill zeros behind its end (and read nothing there: see launch_mm_table).  (Zeroing those lines in
+// shared memory before the MMAs cost every tile a cross-CTA fence: 64 skewed experts, 32768 rows, 1011 us.)
 //
 // Every wait is bounded; one that runs out raises the timeout bit of the status word and the abort flag of
 // every CTA of its cluster, which wind down together.
@@ -989,7 +989,7 @@ mm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
 }
 
 // One thread per expert: its segment from the offsets, and the scan of the row tiles; then, for wgrad,
-// one warp per tensor map: the map of the whole operand with the segment's first row and row count.
+// one warp per tensor map: a one-row map of the operand with the segment's first row and row count.
 __global__ void __launch_bounds__(kMaxGroups) mm_table_kernel(const int32_t* offsets, int E, int64_t rows,
                                                               int tile_rows, MmTable t, WsHeader* hdr,
                                                               const __grid_constant__ MmSegMaps maps) {
@@ -1292,7 +1292,13 @@ cudaError_t launch_mm_table(const int32_t* offsets, int E, int64_t rows, int til
                             WsHeader* hdr, const MmWgradOperands* w, cudaStream_t stream) {
   MmSegMaps maps{};
   if (w != nullptr) {
-    if (make_tma_16(&maps.a, w->a, w->I, rows, 1, kBK) != 0 || make_tma_16(&maps.b, w->b, w->J, rows, 1, kBK) != 0)
+    // Encoded for one row, the fewest a loaded segment has, and given the segment's rows on the device.  Through a map
+    // that the driver encoded for 128 KB or more, a copy reads memory for elements out of bounds too, from the first
+    // 128 KB behind the map's address, which lie inside so large a tensor; through a smaller one it does not.  (Boxes
+    // of 64 rows of 992 bytes with one in bounds: 1.2 KB read a box through maps of up to 132 rows, 16.3 KB
+    // of 133, 131936 bytes; 0.5 KB where such maps share their address.)  Cut down from a map of the whole operand, a
+    // short segment's near the operand's end read up to 128 KB behind it: an illegal address where nothing is mapped.
+    if (make_tma_16(&maps.a, w->a, w->I, 1, 1, kBK) != 0 || make_tma_16(&maps.b, w->b, w->J, 1, 1, kBK) != 0)
       return cudaErrorInvalidValue;
     maps.a_base = w->a;
     maps.b_base = w->b;

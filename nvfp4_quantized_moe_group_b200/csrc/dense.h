@@ -36,7 +36,7 @@ struct MmWgradOperands {
 
 // What the table kernel builds the segments' maps from.
 struct MmSegMaps {
-  CUtensorMap a, b;      // of the whole operands
+  CUtensorMap a, b;      // of the operands' first rows
   const void *a_base, *b_base;
   int64_t a_row_bytes, b_row_bytes;
   CUtensorMap* out;      // nullptr: none
